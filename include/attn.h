@@ -58,7 +58,8 @@ extern "C" {
 typedef enum {
   ATTN_OK = 0,
   ATTN_ERR_INVALID_ARG = 1,   /* bad size, null pointer, Hq % Hkv != 0, scale not finite,
-                                 workspace too small, malformed host cu_seqlens */
+                                 workspace too small, malformed host cu_seqlens; from
+                                 attn_device_status: a paged token without a valid page */
   ATTN_ERR_UNSUPPORTED = 2,   /* D not in {64, 128}, or the device is not sm_100 */
   ATTN_ERR_MISALIGNED = 3,    /* a pointer breaks the alignment rules above */
   ATTN_ERR_CUDA = 4,          /* a CUDA runtime/driver call or a launch failed */
@@ -167,6 +168,95 @@ attn_status attn_decode(const void* q, const void* k_cache, const void* v_cache,
                         int Lmax, int D, float scale, void* workspace, size_t workspace_bytes,
                         void* stream);
 
+/* ---- Paged key/value caches (no page counterpart beyond the 32K-token serving of
+ * attn_decode: the layout that serving many sequences from one pool of memory takes).
+ *
+ * A cache is a pool of num_pages pages of page_size tokens (16, 32, 64, 128 or 256).
+ *   - block_table: DEVICE int32 [B][max_pages]; entry [b][n] is the page of tokens
+ *     n * page_size ... of sequence b.  Entries past a sequence's length are not read.
+ *   - cache_len: DEVICE int32 [B], the cached tokens of each sequence, counting the ones a
+ *     call appends.
+ *   - cu_seqlens: DEVICE int32 [B+1], offsets of the sequences' tokens among the T packed
+ *     ones; NULL: one token per sequence, T = B.  Token i of the n of sequence b stands for
+ *     position cache_len[b] - n + i.  cu_seqlens[B] may be less than T: the rows behind the
+ *     last sequence are neither read as tokens nor written.
+ *   - bf16 pages: k_pages, v_pages [num_pages][page_size][Hkv][D] (a dense cache whose
+ *     sequences' tokens lie in any order of pages).
+ *   - 4-bit pages: one pool of bytes [num_pages][Hkv][page_size / 16][18 * D].  A unit of 16
+ *     tokens of one kv head is
+ *         K codes [16][D / 2], V codes [16][D / 2], K scales [16][D / 64], V scales [16][D / 64]
+ *     with, per group g of 64 elements, a 4-byte scale (bf16 step s in the low half, bf16
+ *     minimum m in the high half); an element's value is s * code + m, code in 0..15.  Of a
+ *     token's 4-byte code words, number (D / 64) * i + g holds elements 64 g + 8 i ... + 7,
+ *     element j of the word at bits 4 j.
+ *   - A token or a length within the call whose place does not exist (a position past the
+ *     table or, with rotation, past rope_len; a page outside 0 ... num_pages - 1) never makes
+ *     a kernel reach outside the pool: the event is recorded, and attn_device_status returns
+ *     ATTN_ERR_INVALID_ARG for it (site codes 0x500 append, 0x501 gather, 0x502 decode, 0x503
+ *     4-bit decode).
+ *   - D in {64, 128}; max_pages * page_size and num_pages * page_size < 2^31 - 512; at most 4096
+ *     heads.  Pointers 16-byte aligned, int32 arrays and lse 4-byte, workspaces 256-byte. */
+
+/* Appends tokens to a paged cache: k, v (and q) are T tokens of Hkv (Hq) heads, bf16, heads
+ * contiguous and tokens *_stride elements apart (multiples of 8), so that they may be slices of
+ * one projection's output.  With rope_cos, rope_sin (fp32 [rope_len][rope_dim / 2]; rope_dim a
+ * multiple of 16 up to D) the first rope_dim elements of every k and q head are rotated by the
+ * angles of the token's position, in fp32 with one rounding to bf16:
+ *     a' = a cos - b sin,  b' = b cos + a sin,   (a, b) = (x[j], x[j + rope_dim / 2])
+ * or (x[2j], x[2j + 1]) if interleaved.  NULL for both: no rotation (then q must be NULL).
+ * q may be NULL (with q_out NULL); q_out [T][Hq][D] is contiguous and may be a contiguous q.
+ * k goes to k_pages and v to v_pages (attn_append_kv) or, as 4 bits, to pages:
+ *     m = min x,  s = bf16((max x - m) / 15),  code = clamp(rint((x - m) / s), 0, 15)
+ * over each group of 64 of the bf16 values that bf16 pages would hold (s = 0: codes 0).  A
+ * group with a NaN or an infinity, or whose range is not finite in fp32, is stored as s = m =
+ * NaN.
+ *   - Tokens behind cu_seqlens[B] and tokens at negative positions are left out silently,
+ *     tokens without a place are left out and recorded: of either, nothing is written.
+ *   - Where two tokens of a call share a place, either's rows may remain.
+ *   - T = 0 does nothing. */
+attn_status attn_append_kv(const void* q, const void* k, const void* v, long long q_stride,
+                           long long k_stride, long long v_stride, const float* rope_cos,
+                           const float* rope_sin, int rope_len, int rope_dim, int interleaved,
+                           const int32_t* cu_seqlens, const int32_t* cache_len,
+                           const int32_t* block_table, void* q_out, void* k_pages, void* v_pages,
+                           int B, int T, int Hq, int Hkv, int D, int max_pages, int num_pages,
+                           int page_size, void* stream);
+attn_status attn_append_kv4(const void* q, const void* k, const void* v, long long q_stride,
+                            long long k_stride, long long v_stride, const float* rope_cos,
+                            const float* rope_sin, int rope_len, int rope_dim, int interleaved,
+                            const int32_t* cu_seqlens, const int32_t* cache_len,
+                            const int32_t* block_table, void* q_out, void* pages, int B, int T,
+                            int Hq, int Hkv, int D, int max_pages, int num_pages, int page_size,
+                            void* stream);
+
+/* Reads tokens back from 4-bit pages as packed bf16 k, v [T][Hkv][D] (attn_fwd's layout): the
+ * last cu_seqlens[b+1] - cu_seqlens[b] tokens of each sequence (NULL: the last one).  Values
+ * are s * code + m in fp32, rounded once.  Tokens at negative positions and tokens without a
+ * place read as zeros; rows behind the last sequence are not written. */
+attn_status attn_gather_kv4(const void* pages, const int32_t* block_table, const int32_t* cache_len,
+                            const int32_t* cu_seqlens, void* k, void* v, int B, int T, int Hkv,
+                            int D, int max_pages, int num_pages, int page_size, void* stream);
+
+/* attn_decode over bf16 pages: the same result from the same kernel, each sequence's cache
+ * found through block_table.  Lengths are clamped to [0, max_pages * page_size].  A page
+ * outside the pool within a sequence's length is recorded and leaves that sequence's o and
+ * lse unspecified.  Sizes, workspace rules and determinism as attn_decode. */
+size_t attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int D, int max_pages, int page_size);
+attn_status attn_decode_paged(const void* q, const void* k_pages, const void* v_pages,
+                              const int32_t* block_table, const int32_t* cache_len, void* o,
+                              float* lse, int B, int Hq, int Hkv, int D, int max_pages,
+                              int num_pages, int page_size, float scale, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* attn_decode over 4-bit pages: the attention over the values the pages stand for.  Codes enter
+ * the products as exact integers and scores are summed in fp32; the weights are rounded to bf16
+ * for the product with V.  Otherwise as attn_decode_paged (workspace rules included). */
+size_t attn_decode_kv4_workspace_size(int B, int Hq, int Hkv, int D, int max_pages, int page_size);
+attn_status attn_decode_kv4(const void* q, const void* pages, const int32_t* block_table,
+                            const int32_t* cache_len, void* o, float* lse, int B, int Hq, int Hkv,
+                            int D, int max_pages, int num_pages, int page_size, float scale,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
 /* Largest number of partial results one attn_merge call combines. */
 #define ATTN_MERGE_MAX_PARTS 16
 
@@ -233,8 +323,9 @@ const char* attn_strerror(attn_status status);
 
 /* Synchronises `stream`, then returns ATTN_ERR_TIMEOUT if any kernel of this library
  * recorded a timed-out wait on the current device since the last call (and clears
- * the record), ATTN_ERR_CUDA if the stream reports a CUDA error, else ATTN_OK.
- * If `site` is not NULL it receives the code of the first wait that timed out. */
+ * the record), ATTN_ERR_INVALID_ARG if one met a paged cache's token or length without a
+ * valid page, ATTN_ERR_CUDA if the stream reports a CUDA error, else ATTN_OK.
+ * If `site` is not NULL it receives the code of the first such wait or token. */
 attn_status attn_device_status(void* stream, unsigned* site);
 
 /* Sets the limit of every device-side wait, in nanoseconds (default 2e9). */

@@ -13,8 +13,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libattn.so")
 SOURCES = ["attn_lib.cu"]
-HEADERS = ["sm100_ptx.cuh", "attn_accum.cuh", "attn_common.cuh", "attn_fwd.cuh", "attn_bwd.cuh", "attn_decode.cuh", "attn_merge.cuh",
-           "attn_relayout.cuh",
+HEADERS = ["sm100_ptx.cuh", "attn_accum.cuh", "attn_append.cuh", "attn_common.cuh", "attn_fwd.cuh", "attn_bwd.cuh",
+           "attn_decode.cuh", "attn_decode4.cuh", "attn_merge.cuh", "attn_page.cuh", "attn_relayout.cuh",
            "umma_selftest.cuh"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

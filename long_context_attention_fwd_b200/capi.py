@@ -43,6 +43,7 @@ _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _fp = ctypes.c_void_p  # float* passed as raw address
 _sz = ctypes.c_size_t
+_ll = ctypes.c_longlong
 
 _SIGNATURES = {
     "attn_fwd": (_i, [_vp, _vp, _vp, _vp, _fp, _i, _i, _i, _i, _i, _i, ctypes.c_float, _vp, _vp]),
@@ -63,6 +64,17 @@ _SIGNATURES = {
     "attn_decode_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "attn_decode": (_i, [_vp, _vp, _vp, _vp, _vp, _fp, _i, _i, _i, _i, _i, ctypes.c_float, _vp,
                          _sz, _vp]),
+    "attn_append_kv": (_i, [_vp, _vp, _vp, _ll, _ll, _ll, _fp, _fp, _i, _i, _i, _vp, _vp, _vp, _vp,
+                            _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _vp]),
+    "attn_append_kv4": (_i, [_vp, _vp, _vp, _ll, _ll, _ll, _fp, _fp, _i, _i, _i, _vp, _vp, _vp, _vp,
+                             _vp, _i, _i, _i, _i, _i, _i, _i, _i, _vp]),
+    "attn_gather_kv4": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp]),
+    "attn_decode_paged_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "attn_decode_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _fp, _i, _i, _i, _i, _i, _i, _i,
+                               ctypes.c_float, _vp, _sz, _vp]),
+    "attn_decode_kv4_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "attn_decode_kv4": (_i, [_vp, _vp, _vp, _vp, _vp, _fp, _i, _i, _i, _i, _i, _i, _i,
+                             ctypes.c_float, _vp, _sz, _vp]),
     "attn_accumulate_bf16": (_i, [_fp, _vp, ctypes.c_longlong, _i, _vp]),
     "attn_convert_f32_bf16": (_i, [_vp, _fp, ctypes.c_longlong, _vp]),
     "attn_transpose_blocks": (_i, [_vp, _vp, ctypes.c_longlong, ctypes.c_longlong,
@@ -163,6 +175,50 @@ def attn_decode(q, k_cache, v_cache, cache_len, o, lse, B, Hq, Hkv, Lmax, D, sca
                 workspace_bytes, stream) -> int:
     return lib().attn_decode(q, k_cache, v_cache, cache_len, o, lse, B, Hq, Hkv, Lmax, D,
                              float(scale), workspace, workspace_bytes, stream)
+
+
+def attn_append_kv(q, k, v, q_stride, k_stride, v_stride, rope_cos, rope_sin, rope_len, rope_dim,
+                   interleaved, cu_seqlens, cache_len, block_table, q_out, k_pages, v_pages, B, T, Hq,
+                   Hkv, D, max_pages, num_pages, page_size, stream) -> int:
+    return lib().attn_append_kv(q, k, v, q_stride, k_stride, v_stride, rope_cos, rope_sin, rope_len,
+                                rope_dim, int(interleaved), cu_seqlens, cache_len, block_table, q_out,
+                                k_pages, v_pages, B, T, Hq, Hkv, D, max_pages, num_pages, page_size,
+                                stream)
+
+
+def attn_append_kv4(q, k, v, q_stride, k_stride, v_stride, rope_cos, rope_sin, rope_len, rope_dim,
+                    interleaved, cu_seqlens, cache_len, block_table, q_out, pages, B, T, Hq, Hkv, D,
+                    max_pages, num_pages, page_size, stream) -> int:
+    return lib().attn_append_kv4(q, k, v, q_stride, k_stride, v_stride, rope_cos, rope_sin, rope_len,
+                                 rope_dim, int(interleaved), cu_seqlens, cache_len, block_table, q_out,
+                                 pages, B, T, Hq, Hkv, D, max_pages, num_pages, page_size, stream)
+
+
+def attn_gather_kv4(pages, block_table, cache_len, cu_seqlens, k, v, B, T, Hkv, D, max_pages,
+                    num_pages, page_size, stream) -> int:
+    return lib().attn_gather_kv4(pages, block_table, cache_len, cu_seqlens, k, v, B, T, Hkv, D,
+                                 max_pages, num_pages, page_size, stream)
+
+
+def attn_decode_paged_workspace_size(B, Hq, Hkv, D, max_pages, page_size) -> int:
+    return lib().attn_decode_paged_workspace_size(B, Hq, Hkv, D, max_pages, page_size)
+
+
+def attn_decode_paged(q, k_pages, v_pages, block_table, cache_len, o, lse, B, Hq, Hkv, D, max_pages,
+                      num_pages, page_size, scale, workspace, workspace_bytes, stream) -> int:
+    return lib().attn_decode_paged(q, k_pages, v_pages, block_table, cache_len, o, lse, B, Hq, Hkv, D,
+                                   max_pages, num_pages, page_size, float(scale), workspace,
+                                   workspace_bytes, stream)
+
+
+def attn_decode_kv4_workspace_size(B, Hq, Hkv, D, max_pages, page_size) -> int:
+    return lib().attn_decode_kv4_workspace_size(B, Hq, Hkv, D, max_pages, page_size)
+
+
+def attn_decode_kv4(q, pages, block_table, cache_len, o, lse, B, Hq, Hkv, D, max_pages, num_pages,
+                    page_size, scale, workspace, workspace_bytes, stream) -> int:
+    return lib().attn_decode_kv4(q, pages, block_table, cache_len, o, lse, B, Hq, Hkv, D, max_pages,
+                                 num_pages, page_size, float(scale), workspace, workspace_bytes, stream)
 
 
 def attn_accumulate_bf16(acc, x, n, init, stream) -> int:

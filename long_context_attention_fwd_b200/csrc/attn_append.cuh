@@ -1,0 +1,289 @@
+// attn_append.cuh -- writing a paged key/value cache, and reading a 4-bit one back.
+//
+// append_kernel takes the new tokens' q, k and v (strided rows of one projection's output, as a
+// rule), turns the first 2 * half elements of q and k by their position's angles,
+//     a' = a cos - b sin,   b' = b cos + a sin      (fp32, one rounding to bf16),
+// with (a, b) = (x[j], x[j + half]) or, interleaved, (x[2j], x[2j + 1]), and writes k and v where
+// the page table says: as bf16, or as 4-bit codes with a step and a minimum per 64 elements,
+//     m = min x,  s = bf16((max x - m) / 15),  code = rint((x - m) / s) in 0..15,
+// of the bf16 values x.  The divisions are IEEE fp32: x - m and s have so few bits that the
+// rounded quotient is on the right side of every half, so the codes are those of exact arithmetic.
+// A group with a NaN or an infinity, or whose range leaves fp32, gets s = m = NaN and reads back
+// as NaN.
+//
+// Bound by HBM: every input element is read once and every output written once.  One block takes
+// a token: D / 16 threads hold a row in two 16-byte chunks, chosen so that rotation partners meet
+// in one thread, and a thread's angles serve every head of the token.  The data loads do not wait
+// for the page table.
+#pragma once
+#include <cuda_bf16.h>
+
+#include "attn_page.cuh"
+
+namespace attn_sm100 {
+namespace append {
+
+constexpr int kThreads = 256;
+constexpr int kAhead = 2;  // rows a thread loads before it waits for the token's place
+
+struct Params {
+  page::PageMap map;
+  const __nv_bfloat16* q;   // nullptr: no queries
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  long long q_stride, k_stride, v_stride;  // elements from one token to the next
+  const float* cos;         // [rope_len][half]; unused when half = 0
+  const float* sin;
+  int rope_len, half, interleaved;
+  int nq, Hkv;              // query heads written (0 without q), kv heads
+  __nv_bfloat16* q_out;     // [T][nq][D]
+  __nv_bfloat16* k_pages;   // bf16 pages
+  __nv_bfloat16* v_pages;
+  uint8_t* pages;           // 4-bit pages
+  unsigned* status;
+};
+
+struct Chunk {
+  float x[8];
+};
+
+__device__ __forceinline__ Chunk unpack(const uint4 u) {
+  Chunk c;
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    c.x[2 * i] = __uint_as_float(w[i] << 16);
+    c.x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+  return c;
+}
+
+__device__ __forceinline__ uint4 pack(const Chunk& c) {
+  return make_uint4(pack_bf16x2(c.x[0], c.x[1]), pack_bf16x2(c.x[2], c.x[3]),
+                    pack_bf16x2(c.x[4], c.x[5]), pack_bf16x2(c.x[6], c.x[7]));
+}
+
+// Products and sums are rounded one by one (no contraction), as a framework's elementwise
+// operations round them.
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+  const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+  a = x;
+}
+
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Eight codes of one word.
+__device__ __forceinline__ uint32_t encode(const Chunk& c, float m, float s) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float t = s > 0.f ? rintf(__fdiv_rn(__fsub_rn(c.x[j], m), s)) : 0.f;
+    w |= uint32_t(fminf(t, 15.f)) << (4 * j);  // t >= 0: m is the group's minimum
+  }
+  return w;
+}
+
+template <int D, bool KV4>
+__global__ void __launch_bounds__(kThreads) append_kernel(const Params p) {
+  constexpr int TPR = D / 16;            // threads of a row
+  constexpr int RPP = kThreads / TPR;    // rows of a pass
+  const int tr = threadIdx.x % TPR;
+  const int r0 = threadIdx.x / TPR;
+  const int rows = p.nq + 2 * p.Hkv;     // a token's rows: q heads, k heads, v heads
+  const int hc = p.half / 8;
+  const bool turned = tr < hc;
+  const int ca = turned ? (p.interleaved ? 2 * tr : tr) : 2 * tr;
+  const int cb = turned && !p.interleaved ? tr + hc : ca + 1;
+
+  auto load = [&](int t, int row, uint4 (&u)[2]) {
+    const __nv_bfloat16* src;
+    if (row < p.nq) src = p.q + t * p.q_stride + row * D;
+    else if (row < p.nq + p.Hkv) src = p.k + t * p.k_stride + (row - p.nq) * D;
+    else src = p.v + t * p.v_stride + (row - p.nq - p.Hkv) * D;
+    u[0] = reinterpret_cast<const uint4*>(src)[ca];  // plain loads: q_out may be q
+    u[1] = reinterpret_cast<const uint4*>(src)[cb];
+  };
+
+  for (int t = blockIdx.x; t < p.map.T; t += gridDim.x) {
+    uint4 u[kAhead][2];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (r0 + i * RPP < rows) load(t, r0 + i * RPP, u[i]);
+
+    int pos, pg, slot;
+    page::Placed st = page::place_token(p.map, t, pos, pg, slot);
+    if (st == page::kFound && p.half > 0 && pos >= p.rope_len) st = page::kBad;
+    if (st == page::kBad && threadIdx.x == 0) page::flag_bad_page(p.status, page::kSiteAppend);
+    if (st != page::kFound) continue;  // the same in every thread of the block
+
+    float c[8], s[8];
+    if (turned) {
+      // chunk tr's and its partner's angles; interleaved, a chunk of 8 elements has 4 angles
+      const long long at = (long long)pos * p.half + 8 * tr;
+      *reinterpret_cast<float4*>(c) = __ldg(reinterpret_cast<const float4*>(p.cos + at));
+      *reinterpret_cast<float4*>(c + 4) = __ldg(reinterpret_cast<const float4*>(p.cos + at) + 1);
+      *reinterpret_cast<float4*>(s) = __ldg(reinterpret_cast<const float4*>(p.sin + at));
+      *reinterpret_cast<float4*>(s + 4) = __ldg(reinterpret_cast<const float4*>(p.sin + at) + 1);
+    }
+
+    for (int base = 0; base < rows; base += kAhead * RPP) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int row = base + i * RPP + r0;
+        const bool live = row < rows;
+        if (base > 0 && live) load(t, row, u[i]);
+        if (!__any_sync(0xffffffffu, live)) continue;
+        if (live && turned && row < p.nq + p.Hkv) {
+          Chunk a = unpack(u[i][0]), b = unpack(u[i][1]);
+          if (p.interleaved) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              turn(a.x[2 * j], a.x[2 * j + 1], c[j], s[j]);
+              turn(b.x[2 * j], b.x[2 * j + 1], c[4 + j], s[4 + j]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) turn(a.x[j], b.x[j], c[j], s[j]);
+          }
+          u[i][0] = pack(a);
+          u[i][1] = pack(b);
+        }
+        if (live && row < p.nq) {
+          uint4* dst = reinterpret_cast<uint4*>(p.q_out + ((long long)t * p.nq + row) * D);
+          dst[ca] = u[i][0];
+          dst[cb] = u[i][1];
+        }
+        const int hv = row - p.nq;                // kv row: K heads, then V heads
+        const bool is_v = hv >= p.Hkv;
+        const int h = is_v ? hv - p.Hkv : hv;
+        if constexpr (!KV4) {
+          if (live && hv >= 0) {
+            const long long tok = ((long long)pg << p.map.log_ps) + slot;
+            uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v_pages : p.k_pages) + (tok * p.Hkv + h) * D);
+            dst[ca] = u[i][0];
+            dst[cb] = u[i][1];
+          }
+        } else {
+          using U = page::Unit<D>;
+          if (!__any_sync(0xffffffffu, live && hv >= 0)) continue;
+          // Minimum and maximum of each group over the row's threads.
+          const Chunk a = unpack(u[i][0]), b = unpack(u[i][1]);
+          const int ga = ca / 8, gb = cb / 8;
+          float lo[U::NG], hi[U::NG];
+#pragma unroll
+          for (int g = 0; g < U::NG; ++g) {
+            lo[g] = INFINITY;
+            hi[g] = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if (ga == g) lo[g] = min_nan(lo[g], a.x[j]), hi[g] = max_nan(hi[g], a.x[j]);
+              if (gb == g) lo[g] = min_nan(lo[g], b.x[j]), hi[g] = max_nan(hi[g], b.x[j]);
+            }
+#pragma unroll
+            for (int o = 1; o < TPR; o <<= 1) {
+              lo[g] = min_nan(lo[g], __shfl_xor_sync(0xffffffffu, lo[g], o));
+              hi[g] = max_nan(hi[g], __shfl_xor_sync(0xffffffffu, hi[g], o));
+            }
+          }
+          uint32_t sm[U::NG];
+          float step[U::NG];
+#pragma unroll
+          for (int g = 0; g < U::NG; ++g) {
+            const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi[g], lo[g]), 15.f));
+            step[g] = __bfloat162float(sb);
+            if (step[g] < INFINITY) {
+              sm[g] = uint32_t(__bfloat16_as_ushort(sb)) | __float_as_uint(lo[g] + 0.f);  // -0 becomes +0
+            } else {
+              step[g] = 0.f;
+              sm[g] = 0x7FC07FC0u;
+            }
+          }
+          if (live && hv >= 0) {
+            const float la = (U::NG == 2 && ga) ? lo[U::NG - 1] : lo[0];
+            const float lb = (U::NG == 2 && gb) ? lo[U::NG - 1] : lo[0];
+            const float sa = (U::NG == 2 && ga) ? step[U::NG - 1] : step[0];
+            const float sb = (U::NG == 2 && gb) ? step[U::NG - 1] : step[0];
+            const int upp_log = p.map.log_ps - 4;
+            uint8_t* unit = p.pages + ((((long long)pg * p.Hkv + h) << upp_log) + (slot >> 4)) * U::BYTES;
+            const int j = slot & 15;
+            uint32_t* code = reinterpret_cast<uint32_t*>(unit + (is_v ? U::OFF_VC : U::OFF_KC) + j * U::CODE);
+            code[U::NG * (ca & 7) + ga] = encode(a, la, sa);
+            code[U::NG * (cb & 7) + gb] = encode(b, lb, sb);
+            if (tr == 0) {
+              uint32_t* sc = reinterpret_cast<uint32_t*>(unit + (is_v ? U::OFF_VS : U::OFF_KS) + j * U::SCALE);
+#pragma unroll
+              for (int g = 0; g < U::NG; ++g) sc[g] = sm[g];
+            }
+          }
+        }
+      }
+    }
+  }
+}
+
+// gather4_kernel: packed token t's K and V out of 4-bit pages, x = s * code + m in fp32 (the
+// product is exact: 8 bits by 4), rounded once to bf16.  One warp takes a token; eight threads
+// hold a row, each the word (or the two words of both groups) of eight elements, so that reads
+// and writes are whole sectors.  Bound by HBM, by the bf16 rows it writes.
+struct GatherParams {
+  page::PageMap map;
+  const uint8_t* pages;
+  int Hkv;
+  __nv_bfloat16* k;  // [T][Hkv][D]
+  __nv_bfloat16* v;
+  unsigned* status;
+};
+
+__device__ __forceinline__ uint4 decode_word(uint32_t w, uint32_t sm) {
+  const float s = __uint_as_float(sm << 16), m = __uint_as_float(sm & 0xffff0000u);
+  Chunk c;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) c.x[j] = fmaf(s, float((w >> (4 * j)) & 15u), m);
+  return pack(c);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) gather4_kernel(const GatherParams p) {
+  using U = page::Unit<D>;
+  const int warp = (blockIdx.x * kThreads + threadIdx.x) >> 5;
+  const int nwarp = gridDim.x * (kThreads / 32);
+  const int lane = threadIdx.x & 31;
+  const int i = lane & 7;                      // words i of each group
+  const int rows = 2 * p.Hkv;
+  for (int t = warp; t < p.map.T; t += nwarp) {
+    int pos, pg, slot;
+    const page::Placed st = page::place_token(p.map, t, pos, pg, slot);
+    if (st == page::kOutside) continue;
+    if (st == page::kBad && lane == 0) page::flag_bad_page(p.status, page::kSiteGather);
+    for (int row = lane >> 3; row < rows; row += 4) {
+      const bool is_v = row >= p.Hkv;
+      const int h = is_v ? row - p.Hkv : row;
+      uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v : p.k) + ((long long)t * p.Hkv + h) * D) + i;
+      if (st != page::kFound) {
+#pragma unroll
+        for (int g = 0; g < U::NG; ++g) dst[8 * g] = make_uint4(0u, 0u, 0u, 0u);
+        continue;
+      }
+      const uint8_t* unit =
+          p.pages + ((((long long)pg * p.Hkv + h) << (p.map.log_ps - 4)) + (slot >> 4)) * U::BYTES;
+      const int j = slot & 15;
+      const uint32_t* code = reinterpret_cast<const uint32_t*>(unit + (is_v ? U::OFF_VC : U::OFF_KC) + j * U::CODE);
+      const uint32_t* sc = reinterpret_cast<const uint32_t*>(unit + (is_v ? U::OFF_VS : U::OFF_KS) + j * U::SCALE);
+#pragma unroll
+      for (int g = 0; g < U::NG; ++g) dst[8 * g] = decode_word(code[U::NG * i + g], sc[g]);
+    }
+  }
+}
+
+}  // namespace append
+}  // namespace attn_sm100

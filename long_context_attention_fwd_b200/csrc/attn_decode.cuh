@@ -26,6 +26,11 @@
 // the rows of the last V tile past the length are zeroed in shared memory before its PV
 // product (whatever the cache holds there, 0 * NaN would otherwise poison O).
 //
+// PAGED: the cache lies in pages (attn_page.cuh) and a tile is loaded page by page, a box of up
+// to 128 rows each; everything after the loads is the same.  The producer warp's lanes look up
+// the next tile's pages while the current tile's loads wait for room, and each issues its own
+// page's loads.  A page of the table that is not in the pool is recorded and loads zeros.
+//
 // Each CTA first combines its two streams into one partial (o_s, lse_s).  The last CTA of
 // a (sequence, kv head) to finish then combines the partials of every split into o and
 // lse (the exact log-sum-exp rule of attn_merge), so a decode step is one launch.  The
@@ -38,6 +43,7 @@
 #pragma once
 #include <cuda_bf16.h>
 #include "attn_merge.cuh"
+#include "attn_page.cuh"
 #include "sm100_ptx.cuh"
 
 namespace attn_sm100 {
@@ -70,6 +76,8 @@ struct Params {
   float scale_log2;
   unsigned* status;
   unsigned long long timeout_ns;
+  const int32_t* table;      // PAGED: [B][width] pages of 2^log_ps tokens; Lmax = width << log_ps
+  int width, num_pages, log_ps;
 };
 
 template <int D>
@@ -168,7 +176,7 @@ __device__ void merge_rows(const Params& p, int row0, int G, int nparts, uint8_t
   }
 }
 
-template <int D>
+template <int D, bool PAGED = false>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const Params p) {
@@ -261,6 +269,46 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       mbar_arrive_expect_tx(q_full, C::QT_BYTES);
       for (int hf = 0; hf < D / 64; ++hf)
         tma_load_3d(&tm_q, q_full, smem + C::OFF_Q + hf * kSlab, hf * 64, 0, row0);
+    }
+    if constexpr (PAGED) {
+      const int rows_log = min(p.log_ps, 7);            // tokens of one box
+      const int nseg = BN >> rows_log;                  // boxes of a tile (at most 8)
+      const uint32_t seg_bytes = uint32_t(D * 2) << rows_log;
+      const int pool = p.num_pages << p.log_ps;         // one past the pool: reads zeros
+      // Token coordinate of this lane's box of tile j, or -1 past the sequence's length.
+      auto locate = [&](int j) {
+        const int tok = (j0 + j) * BN + (lane << rows_log);
+        if (j >= n || lane >= nseg || tok >= L) return -1;
+        const int pg = __ldg(p.table + (long long)b * p.width + (tok >> p.log_ps));
+        if (pg < 0 || pg >= p.num_pages) {
+          page::flag_bad_page(p.status, page::kSiteDecode);
+          return pool;
+        }
+        return (pg << p.log_ps) + (tok & ((1 << p.log_ps) - 1));
+      };
+      auto load = [&](const CUtensorMap* tm, uint64_t* bar, int off, int st, int coord, uint32_t bytes) {
+        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+        __syncwarp();
+        if (coord >= 0)
+          for (int hf = 0; hf < D / 64; ++hf)
+            tma_load_3d(tm, bar, smem + off + st * C::KV_BYTES + hf * kSlab + ((lane << rows_log) * 128),
+                        hf * 64, g, coord);
+      };
+      int next = locate(0);
+      for (int j = 0; j < n; ++j) {
+        const int st = j % C::NS;
+        const uint32_t ph = (j / C::NS) & 1;
+        const int coord = next;
+        const uint32_t bytes = seg_bytes * uint32_t(__popc(__ballot_sync(0xffffffffu, coord >= 0)));
+        next = locate(j + 1);
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&k_empty[st], ph ^ 1, wc, kSiteKEmpty)))) break;
+        load(&tm_k, &k_full[st], C::OFF_K, st, coord, bytes);
+        ++nk;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&v_empty[st], ph ^ 1, wc, kSiteVEmpty)))) break;
+        load(&tm_v, j < n_plain_v ? &v_full[st] : v_raw, C::OFF_V, st, coord, bytes);
+        if (j < n_plain_v) ++nv;
+      }
+    } else if (lane == 0) {
       for (int j = 0; j < n && ok; ++j) {
         const int st = j % C::NS;
         const uint32_t ph = (j / C::NS) & 1;

@@ -15,8 +15,10 @@
 
 #include "../../include/attn.h"
 #include "attn_accum.cuh"
+#include "attn_append.cuh"
 #include "attn_bwd.cuh"
 #include "attn_decode.cuh"
+#include "attn_decode4.cuh"
 #include "attn_fwd.cuh"
 #include "attn_merge.cuh"
 #include "attn_relayout.cuh"
@@ -166,23 +168,31 @@ attn_status device_setup(DeviceState** out, const void* ptr = nullptr) {
       e = e ? e : cudaFuncSetAttribute(bwd::attn_bwd_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, bwd::Cfg<128>::SMEM_ALLOC);
       e = e ? e : cudaFuncSetAttribute(decode::attn_decode_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, decode::Cfg<64>::SMEM_ALLOC);
       e = e ? e : cudaFuncSetAttribute(decode::attn_decode_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, decode::Cfg<128>::SMEM_ALLOC);
+      e = e ? e : cudaFuncSetAttribute(decode::attn_decode_kernel<64, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, decode::Cfg<64>::SMEM_ALLOC);
+      e = e ? e : cudaFuncSetAttribute(decode::attn_decode_kernel<128, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, decode::Cfg<128>::SMEM_ALLOC);
+      e = e ? e : cudaFuncSetAttribute(decode4::attn_decode4_kernel<64, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, decode4::Cfg<64, 1>::SMEM_BYTES);
+      e = e ? e : cudaFuncSetAttribute(decode4::attn_decode4_kernel<64, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, decode4::Cfg<64, 2>::SMEM_BYTES);
+      e = e ? e : cudaFuncSetAttribute(decode4::attn_decode4_kernel<128, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, decode4::Cfg<128, 1>::SMEM_BYTES);
+      e = e ? e : cudaFuncSetAttribute(decode4::attn_decode4_kernel<128, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, decode4::Cfg<128, 2>::SMEM_BYTES);
       e = e ? e : cudaFuncSetAttribute(selftest::umma_selftest_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, 32768 + 128 * 64 * 2 + 2048);
       e = e ? e : cudaFuncSetAttribute(selftest::umma_selftest_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, 32768 + 128 * 128 * 2 + 2048);
       if (e != cudaSuccess) return fail_cuda("cudaFuncSetAttribute", e);
       // The kernels re-split registers between warpgroups with setmaxnreg; that is only
       // safe when each thread starts with exactly the budget the split was sized for.
-      const void* split_kernels[7] = {
+      const void* split_kernels[9] = {
           reinterpret_cast<const void*>(fwd::attn_fwd_kernel<64>),
           reinterpret_cast<const void*>(fwd::attn_fwd_kernel<128>),
           reinterpret_cast<const void*>(fwd::attn_fwd_kernel<128, true>),
           reinterpret_cast<const void*>(bwd::attn_bwd_kernel<64>),
           reinterpret_cast<const void*>(bwd::attn_bwd_kernel<128>),
           reinterpret_cast<const void*>(decode::attn_decode_kernel<64>),
-          reinterpret_cast<const void*>(decode::attn_decode_kernel<128>)};
-      const int split_regs[7] = {fwd::kRegsLaunch, fwd::kRegsLaunch, fwd::kRegsLaunch,
+          reinterpret_cast<const void*>(decode::attn_decode_kernel<128>),
+          reinterpret_cast<const void*>(decode::attn_decode_kernel<64, true>),
+          reinterpret_cast<const void*>(decode::attn_decode_kernel<128, true>)};
+      const int split_regs[9] = {fwd::kRegsLaunch, fwd::kRegsLaunch, fwd::kRegsLaunch,
                                  bwd::kRegsLaunch, bwd::kRegsLaunch, decode::kRegsLaunch,
-                                 decode::kRegsLaunch};
-      for (int i = 0; i < 7; ++i) {
+                                 decode::kRegsLaunch, decode::kRegsLaunch, decode::kRegsLaunch};
+      for (int i = 0; i < 9; ++i) {
         cudaFuncAttributes fa;
         if ((e = cudaFuncGetAttributes(&fa, split_kernels[i])) != cudaSuccess)
           return fail_cuda("cudaFuncGetAttributes", e);
@@ -225,11 +235,12 @@ attn_status device_setup(DeviceState** out, const void* ptr = nullptr) {
   return ATTN_OK;
 }
 
-// 3-D view (D, H, T) of a [T][H][D] bf16 tensor; box 64 x 1 x 128, 128-byte swizzle.
-attn_status make_map(CUtensorMap* m, const void* base, int D, int H, long long T) {
+// 3-D view (D, H, T) of a [T][H][D] bf16 tensor; box 64 x 1 x rows, 128-byte swizzle.
+attn_status make_map(CUtensorMap* m, const void* base, int D, int H, long long T,
+                     unsigned rows = 128) {
   const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(T)};
   const cuuint64_t strides[2] = {cuuint64_t(D) * 2, cuuint64_t(H) * D * 2};
-  const cuuint32_t box[3] = {64, 1, 128};
+  const cuuint32_t box[3] = {64, 1, rows};
   const cuuint32_t es[3] = {1, 1, 1};
   const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
                               strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -372,11 +383,131 @@ attn_status check_decode_sizes(int B, int Hq, int Hkv, int Lmax, int D, float sc
   return ATTN_OK;
 }
 
+decode::Params decode_params(const DecodeWs& w, const void* q, void* o, float* lse,
+                             const int32_t* cache_len, void* workspace, int B, int Hq, int Hkv,
+                             int Lmax, float scale, const DeviceState& dev) {
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  decode::Params p{};
+  p.cache_len = cache_len;
+  p.o_part = reinterpret_cast<__nv_bfloat16*>(ws + w.o_part);
+  p.lse_part = reinterpret_cast<float*>(ws + w.lse_part);
+  p.Hq = Hq;
+  p.G = Hq / Hkv;
+  p.Hkv = Hkv;
+  p.Lmax = Lmax;
+  p.nsplit = w.nsplit;
+  p.tps = w.tps;
+  p.rows = B * Hq;
+  p.flags = reinterpret_cast<unsigned long long*>(ws + w.flags);
+  p.tag = next_decode_tag();
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.status = dev.status;
+  p.timeout_ns = g_timeout_ns.load();
+  return p;
+}
+
+// ---- paged caches
+constexpr int kMaxHeads = 4096;  // keeps a token's row offsets in 32 bits
+
+attn_status check_pages(int B, int max_pages, int num_pages, int page_size, int* log_ps) {
+  if (B < 1 || max_pages < 1 || num_pages < 1) return ATTN_ERR_INVALID_ARG;
+  int l = 4;
+  while (l < 8 && (1 << l) < page_size) ++l;
+  if ((1 << l) != page_size) return ATTN_ERR_INVALID_ARG;
+  // token indices of the pool and of a sequence are int32 in the kernels
+  if (((long long)max_pages << l) >= (1ll << 31) - 512 || ((long long)num_pages << l) >= (1ll << 31) - 512)
+    return ATTN_ERR_INVALID_ARG;
+  *log_ps = l;
+  return ATTN_OK;
+}
+
+attn_status page_map(page::PageMap* m, const int32_t* block_table, const int32_t* cache_len,
+                     const int32_t* cu_seqlens, int B, int T, int max_pages, int num_pages,
+                     int page_size) {
+  int log_ps = 0;
+  const attn_status st = check_pages(B, max_pages, num_pages, page_size, &log_ps);
+  if (st != ATTN_OK) return st;
+  if (T < 0 || T >= (1ll << 31) - 512 || (!cu_seqlens && T != B)) return ATTN_ERR_INVALID_ARG;
+  if (!block_table || !cache_len) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(block_table, 4) || !aligned(cache_len, 4) || (cu_seqlens && !aligned(cu_seqlens, 4)))
+    return ATTN_ERR_MISALIGNED;
+  *m = page::PageMap{block_table, cache_len, cu_seqlens, B, T, max_pages, num_pages, log_ps};
+  return ATTN_OK;
+}
+
+// The checks and parameters the two appends share.
+attn_status append_params(append::Params* p, const void* q, const void* k, const void* v,
+                          long long q_stride, long long k_stride, long long v_stride,
+                          const float* rope_cos, const float* rope_sin, int rope_len, int rope_dim,
+                          int interleaved, const int32_t* cu_seqlens, const int32_t* cache_len,
+                          const int32_t* block_table, void* q_out, int B, int T, int Hq, int Hkv,
+                          int D, int max_pages, int num_pages, int page_size) {
+  const attn_status st = page_map(&p->map, block_table, cache_len, cu_seqlens, B, T, max_pages, num_pages, page_size);
+  if (st != ATTN_OK) return st;
+  if (Hkv < 1 || Hkv > kMaxHeads || (q && (Hq < 1 || Hq > kMaxHeads))) return ATTN_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+  if (T > 0 && (!k || !v)) return ATTN_ERR_INVALID_ARG;
+  if ((q != nullptr) != (q_out != nullptr)) return ATTN_ERR_INVALID_ARG;
+  if ((rope_cos != nullptr) != (rope_sin != nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (rope_cos) {
+    if (rope_len < 1 || rope_dim < 16 || rope_dim > D || rope_dim % 16) return ATTN_ERR_INVALID_ARG;
+  } else if (q) {
+    return ATTN_ERR_INVALID_ARG;  // queries only come along to be turned
+  }
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
+      !aligned(rope_cos, 16) || !aligned(rope_sin, 16) || q_stride % 8 || k_stride % 8 || v_stride % 8)
+    return ATTN_ERR_MISALIGNED;
+  p->q = static_cast<const __nv_bfloat16*>(q);
+  p->k = static_cast<const __nv_bfloat16*>(k);
+  p->v = static_cast<const __nv_bfloat16*>(v);
+  p->q_stride = q_stride;
+  p->k_stride = k_stride;
+  p->v_stride = v_stride;
+  p->cos = rope_cos;
+  p->sin = rope_sin;
+  p->rope_len = rope_len;
+  p->half = rope_cos ? rope_dim / 2 : 0;
+  p->interleaved = interleaved ? 1 : 0;
+  p->nq = q ? Hq : 0;
+  p->Hkv = Hkv;
+  p->q_out = static_cast<__nv_bfloat16*>(q_out);
+  return ATTN_OK;
+}
+
+unsigned grid_of(long long need, unsigned most) { return unsigned(need < most ? need : most); }
+
+// Plan of the 4-bit decode: one block per SM, fewer where the longest possible batch has no
+// tile for every warp.  Up to 8 query heads of a kv head take one pass of 8, more take passes
+// of 16.  The workspace holds two shared parts per block.
+struct Decode4Ws {
+  size_t ml_part, flags, total;
+  long long tiles;
+  int nt, passes;
+  unsigned grid;
+};
+Decode4Ws decode4_ws(int B, int Hq, int Hkv, int D, int Lmax) {
+  Decode4Ws w;
+  const int G = Hq / Hkv;
+  w.nt = G <= 8 ? 1 : 2;
+  const int heads = 8 * w.nt;
+  const int warps = w.nt == 1 ? decode4::Cfg<128, 1>::W : decode4::Cfg<128, 2>::W;
+  w.passes = (G + heads - 1) / heads;
+  w.tiles = (long long)((Lmax + decode4::kTile - 1) / decode4::kTile) * B * Hkv * w.passes;
+  w.grid = grid_of((w.tiles + warps - 1) / warps, kPlanSMs);
+  const size_t parts = 2 * size_t(w.grid) * heads;
+  w.ml_part = round_up(parts * D * sizeof(float), 256);
+  w.flags = w.ml_part + round_up(parts * 2 * sizeof(float), 256);
+  w.total = w.flags + round_up(2 * size_t(w.grid) * 8, 256);
+  return w;
+}
+
 }  // namespace
 
 extern "C" {
 
-int attn_version(void) { return 100; }
+int attn_version(void) { return 101; }
 
 const char* attn_last_error(void) { return g_last_error; }
 
@@ -644,25 +775,7 @@ attn_status attn_decode(const void* q, const void* k_cache, const void* v_cache,
   if (make_map(&mq, q, D, 1, (long long)B * Hq) || make_map(&mk, k_cache, D, Hkv, (long long)B * Lmax) ||
       make_map(&mv, v_cache, D, Hkv, (long long)B * Lmax))
     return ATTN_ERR_CUDA;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  decode::Params p;
-  p.cache_len = cache_len;
-  p.o_part = reinterpret_cast<__nv_bfloat16*>(ws + w.o_part);
-  p.lse_part = reinterpret_cast<float*>(ws + w.lse_part);
-  p.Hq = Hq;
-  p.G = Hq / Hkv;
-  p.Hkv = Hkv;
-  p.Lmax = Lmax;
-  p.nsplit = w.nsplit;
-  p.tps = w.tps;
-  p.rows = B * Hq;
-  p.flags = reinterpret_cast<unsigned long long*>(ws + w.flags);
-  p.tag = next_decode_tag();
-  p.o = static_cast<__nv_bfloat16*>(o);
-  p.lse = lse;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.status = dev->status;
-  p.timeout_ns = g_timeout_ns.load();
+  decode::Params p = decode_params(w, q, o, lse, cache_len, workspace, B, Hq, Hkv, Lmax, scale, *dev);
   const long long nblocks = (long long)B * Hkv * w.nsplit;
   if (nblocks >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -671,6 +784,197 @@ attn_status attn_decode(const void* q, const void* k_cache, const void* v_cache,
   else
     decode::attn_decode_kernel<128><<<unsigned(nblocks), decode::kThreads, decode::Cfg<128>::SMEM_ALLOC, s>>>(mq, mk, mv, p);
   return check_launch("attn_decode_kernel launch");
+}
+
+size_t attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int D, int max_pages, int page_size) {
+  int log_ps = 0;
+  if (check_pages(B, max_pages, 1, page_size, &log_ps) != ATTN_OK) return 0;
+  return attn_decode_workspace_size(B, Hq, Hkv, max_pages << log_ps, D);
+}
+
+attn_status attn_decode_paged(const void* q, const void* k_pages, const void* v_pages,
+                              const int32_t* block_table, const int32_t* cache_len, void* o,
+                              float* lse, int B, int Hq, int Hkv, int D, int max_pages,
+                              int num_pages, int page_size, float scale, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  DeviceRestore restore_device;
+  int log_ps = 0;
+  attn_status st = check_pages(B, max_pages, num_pages, page_size, &log_ps);
+  if (st != ATTN_OK) return st;
+  const int Lmax = max_pages << log_ps;
+  if ((st = check_decode_sizes(B, Hq, Hkv, Lmax, D, scale)) != ATTN_OK) return st;
+  if (!q || !k_pages || !v_pages || !block_table || !cache_len || !o || !lse || !workspace)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(o, 16) ||
+      !aligned(workspace, 256) || !aligned(lse, 4) || !aligned(cache_len, 4) ||
+      !aligned(block_table, 4))
+    return ATTN_ERR_MISALIGNED;
+  const DecodeWs w = decode_ws(B, Hq, Hkv, Lmax, D);
+  if (workspace_bytes < w.total) return ATTN_ERR_INVALID_ARG;
+  const long long nblocks = (long long)B * Hkv * w.nsplit;
+  if (nblocks >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
+  DeviceState* dev = nullptr;
+  if ((st = device_setup(&dev, q)) != ATTN_OK) return st;
+
+  CUtensorMap mq, mk, mv;
+  const long long T = (long long)num_pages << log_ps;
+  const unsigned rows = page_size < 128 ? unsigned(page_size) : 128u;
+  if (make_map(&mq, q, D, 1, (long long)B * Hq) || make_map(&mk, k_pages, D, Hkv, T, rows) ||
+      make_map(&mv, v_pages, D, Hkv, T, rows))
+    return ATTN_ERR_CUDA;
+  decode::Params p = decode_params(w, q, o, lse, cache_len, workspace, B, Hq, Hkv, Lmax, scale, *dev);
+  p.table = block_table;
+  p.width = max_pages;
+  p.num_pages = num_pages;
+  p.log_ps = log_ps;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (D == 64)
+    decode::attn_decode_kernel<64, true><<<unsigned(nblocks), decode::kThreads, decode::Cfg<64>::SMEM_ALLOC, s>>>(mq, mk, mv, p);
+  else
+    decode::attn_decode_kernel<128, true><<<unsigned(nblocks), decode::kThreads, decode::Cfg<128>::SMEM_ALLOC, s>>>(mq, mk, mv, p);
+  return check_launch("attn_decode_kernel (paged) launch");
+}
+
+size_t attn_decode_kv4_workspace_size(int B, int Hq, int Hkv, int D, int max_pages, int page_size) {
+  int log_ps = 0;
+  if (check_pages(B, max_pages, 1, page_size, &log_ps) != ATTN_OK) return 0;
+  if (check_decode_sizes(B, Hq, Hkv, max_pages << log_ps, D, 1.f) != ATTN_OK) return 0;
+  return decode4_ws(B, Hq, Hkv, D, max_pages << log_ps).total;
+}
+
+attn_status attn_decode_kv4(const void* q, const void* pages, const int32_t* block_table,
+                            const int32_t* cache_len, void* o, float* lse, int B, int Hq, int Hkv,
+                            int D, int max_pages, int num_pages, int page_size, float scale,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  DeviceRestore restore_device;
+  int log_ps = 0;
+  attn_status st = check_pages(B, max_pages, num_pages, page_size, &log_ps);
+  if (st != ATTN_OK) return st;
+  const int Lmax = max_pages << log_ps;
+  if ((st = check_decode_sizes(B, Hq, Hkv, Lmax, D, scale)) != ATTN_OK) return st;
+  if (!q || !pages || !block_table || !cache_len || !o || !lse || !workspace)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(pages, 16) || !aligned(o, 16) || !aligned(workspace, 256) ||
+      !aligned(lse, 4) || !aligned(cache_len, 4) || !aligned(block_table, 4))
+    return ATTN_ERR_MISALIGNED;
+  const Decode4Ws w = decode4_ws(B, Hq, Hkv, D, Lmax);
+  if (w.tiles >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
+  if (workspace_bytes < w.total) return ATTN_ERR_INVALID_ARG;
+  DeviceState* dev = nullptr;
+  if ((st = device_setup(&dev, q)) != ATTN_OK) return st;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  decode4::Params p;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.pages = static_cast<const uint8_t*>(pages);
+  p.table = block_table;
+  p.cache_len = cache_len;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.RB = w.passes;
+  p.width = max_pages;
+  p.num_pages = num_pages;
+  p.log_ps = log_ps;
+  p.o_part = reinterpret_cast<float*>(ws);
+  p.ml_part = reinterpret_cast<float*>(ws + w.ml_part);
+  p.flags = reinterpret_cast<unsigned long long*>(ws + w.flags);
+  p.tag = next_decode_tag();
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.status = dev->status;
+  p.timeout_ns = g_timeout_ns.load();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto launch = [&](auto kernel, auto cfg) {
+    kernel<<<w.grid, cfg.THREADS, cfg.SMEM_BYTES, s>>>(p);
+  };
+  if (D == 64 && w.nt == 1) launch(decode4::attn_decode4_kernel<64, 1>, decode4::Cfg<64, 1>{});
+  else if (D == 64) launch(decode4::attn_decode4_kernel<64, 2>, decode4::Cfg<64, 2>{});
+  else if (w.nt == 1) launch(decode4::attn_decode4_kernel<128, 1>, decode4::Cfg<128, 1>{});
+  else launch(decode4::attn_decode4_kernel<128, 2>, decode4::Cfg<128, 2>{});
+  return check_launch("attn_decode4_kernel launch");
+}
+
+attn_status attn_append_kv(const void* q, const void* k, const void* v, long long q_stride,
+                           long long k_stride, long long v_stride, const float* rope_cos,
+                           const float* rope_sin, int rope_len, int rope_dim, int interleaved,
+                           const int32_t* cu_seqlens, const int32_t* cache_len,
+                           const int32_t* block_table, void* q_out, void* k_pages, void* v_pages,
+                           int B, int T, int Hq, int Hkv, int D, int max_pages, int num_pages,
+                           int page_size, void* stream) {
+  DeviceRestore restore_device;
+  append::Params p{};
+  attn_status st = append_params(&p, q, k, v, q_stride, k_stride, v_stride, rope_cos, rope_sin,
+                                 rope_len, rope_dim, interleaved, cu_seqlens, cache_len,
+                                 block_table, q_out, B, T, Hq, Hkv, D, max_pages, num_pages, page_size);
+  if (st != ATTN_OK) return st;
+  if (!k_pages || !v_pages) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(k_pages, 16) || !aligned(v_pages, 16)) return ATTN_ERR_MISALIGNED;
+  if (T == 0) return ATTN_OK;
+  DeviceState* dev = nullptr;
+  if ((st = device_setup(&dev, k)) != ATTN_OK) return st;
+  p.k_pages = static_cast<__nv_bfloat16*>(k_pages);
+  p.v_pages = static_cast<__nv_bfloat16*>(v_pages);
+  p.status = dev->status;
+  const unsigned grid = grid_of(T, dev->sms * 8);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (D == 64) append::append_kernel<64, false><<<grid, append::kThreads, 0, s>>>(p);
+  else append::append_kernel<128, false><<<grid, append::kThreads, 0, s>>>(p);
+  return check_launch("append_kernel launch");
+}
+
+attn_status attn_append_kv4(const void* q, const void* k, const void* v, long long q_stride,
+                            long long k_stride, long long v_stride, const float* rope_cos,
+                            const float* rope_sin, int rope_len, int rope_dim, int interleaved,
+                            const int32_t* cu_seqlens, const int32_t* cache_len,
+                            const int32_t* block_table, void* q_out, void* pages, int B, int T,
+                            int Hq, int Hkv, int D, int max_pages, int num_pages, int page_size,
+                            void* stream) {
+  DeviceRestore restore_device;
+  append::Params p{};
+  attn_status st = append_params(&p, q, k, v, q_stride, k_stride, v_stride, rope_cos, rope_sin,
+                                 rope_len, rope_dim, interleaved, cu_seqlens, cache_len,
+                                 block_table, q_out, B, T, Hq, Hkv, D, max_pages, num_pages, page_size);
+  if (st != ATTN_OK) return st;
+  if (!pages) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(pages, 16)) return ATTN_ERR_MISALIGNED;
+  if (T == 0) return ATTN_OK;
+  DeviceState* dev = nullptr;
+  if ((st = device_setup(&dev, k)) != ATTN_OK) return st;
+  p.pages = static_cast<uint8_t*>(pages);
+  p.status = dev->status;
+  const unsigned grid = grid_of(T, dev->sms * 8);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (D == 64) append::append_kernel<64, true><<<grid, append::kThreads, 0, s>>>(p);
+  else append::append_kernel<128, true><<<grid, append::kThreads, 0, s>>>(p);
+  return check_launch("append_kernel (4-bit) launch");
+}
+
+attn_status attn_gather_kv4(const void* pages, const int32_t* block_table, const int32_t* cache_len,
+                            const int32_t* cu_seqlens, void* k, void* v, int B, int T, int Hkv,
+                            int D, int max_pages, int num_pages, int page_size, void* stream) {
+  DeviceRestore restore_device;
+  append::GatherParams p{};
+  attn_status st = page_map(&p.map, block_table, cache_len, cu_seqlens, B, T, max_pages, num_pages, page_size);
+  if (st != ATTN_OK) return st;
+  if (Hkv < 1 || Hkv > kMaxHeads) return ATTN_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+  if (T == 0) return ATTN_OK;
+  if (!pages || !k || !v) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(pages, 16) || !aligned(k, 16) || !aligned(v, 16)) return ATTN_ERR_MISALIGNED;
+  DeviceState* dev = nullptr;
+  if ((st = device_setup(&dev, k)) != ATTN_OK) return st;
+  p.pages = static_cast<const uint8_t*>(pages);
+  p.Hkv = Hkv;
+  p.k = static_cast<__nv_bfloat16*>(k);
+  p.v = static_cast<__nv_bfloat16*>(v);
+  p.status = dev->status;
+  const unsigned grid = grid_of((T + append::kThreads / 32 - 1) / (append::kThreads / 32), dev->sms * 8);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (D == 64) append::gather4_kernel<64><<<grid, append::kThreads, 0, s>>>(p);
+  else append::gather4_kernel<128><<<grid, append::kThreads, 0, s>>>(p);
+  return check_launch("gather4_kernel launch");
 }
 
 attn_status attn_accumulate_bf16(float* acc, const void* x, long long n, int init, void* stream) {
@@ -752,7 +1056,8 @@ attn_status attn_device_status(void* stream, unsigned* site) {
   const unsigned zero[2] = {0, 0};
   if ((e = cudaMemcpy(dev->status, zero, sizeof(zero), cudaMemcpyHostToDevice)) != cudaSuccess)
     return fail_cuda("cudaMemcpy(status reset)", e);
-  return (word[0] & kStatusTimeout) ? ATTN_ERR_TIMEOUT : ATTN_ERR_CUDA;
+  if (word[0] & kStatusTimeout) return ATTN_ERR_TIMEOUT;
+  return (word[0] & page::kStatusBadPage) ? ATTN_ERR_INVALID_ARG : ATTN_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -8,6 +8,15 @@
     o, lse = attn_decode(q, k_cache, v_cache, cache_len)       # one new token per sequence
     o, lse = attn_fwd_fp8(q8, k8, v8, qd, kd, vd)              # e4m3 inputs + descale factors
 
+Serving from a paged cache, in bf16 or in 4 bits (cache_len counts the new tokens too):
+
+    q = attn_append_kv(k, v, k_pages, v_pages, table, cache_len, q=q, rope=(cos, sin))
+    o, lse = attn_decode_paged(q, k_pages, v_pages, table, cache_len)
+    pages = kv4_pages(num_pages, page_size, Hkv, D)            # the 4-bit pool
+    q = attn_append_kv4(k, v, pages, table, cache_len, q=q, rope=(cos, sin))
+    o, lse = attn_decode_kv4(q, pages, table, cache_len)
+    k, v = attn_gather_kv4(pages, table, cache_len, cu, T)     # cached tokens back as bf16
+
 All arithmetic runs in libattn.so; these functions only check shapes, allocate
 outputs with torch and pass raw pointers and the current CUDA stream.
 """
@@ -278,6 +287,267 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                           cache_len.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Lmax,
                           D, scale, workspace.data_ptr(), ws_bytes, _stream(q.device))
     capi.check(st, "attn_decode")
+    return out, lse
+
+
+# ---------------------------------------------------------------- paged key/value caches
+KV4_UNIT = 16  # tokens of a unit of 4-bit pages
+
+
+def kv4_pages(num_pages: int, page_size: int, Hkv: int, D: int, device="cuda") -> torch.Tensor:
+    """A pool of 4-bit pages: uint8 [num_pages, Hkv, page_size / 16, 18 D] (contents unset).
+    include/attn.h describes the bytes of a unit of 16 tokens."""
+    if page_size not in (16, 32, 64, 128, 256) or D not in (64, 128):
+        raise ValueError("page_size must be 16, 32, 64, 128 or 256 and D 64 or 128")
+    return torch.empty((num_pages, Hkv, page_size // KV4_UNIT, 18 * D), dtype=torch.uint8, device=device)
+
+
+def _check_kv4(pages: torch.Tensor):
+    """(num_pages, Hkv, page_size, D) of a pool of 4-bit pages."""
+    if not pages.is_cuda:
+        raise ValueError("libattn needs CUDA tensors (there is no CPU path)")
+    if pages.dim() != 4 or pages.dtype != torch.uint8 or pages.shape[3] not in (18 * 64, 18 * 128) \
+            or not pages.is_contiguous():
+        raise ValueError("pages must be contiguous uint8 [num_pages, Hkv, page_size / 16, 18 D]")
+    P, Hkv, units, row = pages.shape
+    return P, Hkv, units * KV4_UNIT, row // 18
+
+
+def _check_paged(k_pages: torch.Tensor, v_pages: torch.Tensor):
+    """(num_pages, Hkv, page_size, D) of a pool of bf16 pages."""
+    _check_inputs(k_pages, v_pages)
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must be [num_pages, page_size, Hkv, D]")
+    P, ps, Hkv, D = k_pages.shape
+    return P, Hkv, ps, D
+
+
+def _check_int32(t: torch.Tensor, name: str, dim: int) -> None:
+    if t.dtype != torch.int32 or not t.is_cuda or t.dim() != dim or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dim}-D int32 CUDA tensor")
+
+
+def _check_map(block_table, cache_len, cu_seqlens, device) -> int:
+    """Checks the arrays that place tokens; returns the number of sequences."""
+    _check_int32(block_table, "block_table", 2)
+    _check_int32(cache_len, "cache_len", 1)
+    B = cache_len.shape[0]
+    if block_table.shape[0] != B:
+        raise ValueError("block_table needs a row for each entry of cache_len")
+    if cu_seqlens is not None:
+        _check_int32(cu_seqlens, "cu_seqlens", 1)
+        if cu_seqlens.shape[0] != B + 1:
+            raise ValueError("cu_seqlens needs one entry more than cache_len")
+    _same_device(device, block_table, cache_len, cu_seqlens)
+    return B
+
+
+def _check_rows(t: torch.Tensor, name: str, T: int, H: int, D: int, device) -> None:
+    """A [T, H, D] bf16 tensor whose tokens may lie any multiple of 8 elements apart (a
+    slice of a projection that holds q, k and v side by side)."""
+    if t.dtype != torch.bfloat16:
+        raise ValueError("tensors must be bfloat16")
+    if tuple(t.shape) != (T, H, D) or t.device != device:
+        raise ValueError(f"{name} must be {(T, H, D)} on {device}")
+    if T and (t.stride(2) != 1 or (H > 1 and t.stride(1) != D) or (T > 1 and t.stride(0) % 8)):
+        raise ValueError(f"{name}: heads must be contiguous and tokens a multiple of 8 elements apart")
+
+
+def _append_args(k, v, block_table, cache_len, q, rope, cu_seqlens, q_out, Hkv, D, device):
+    """Checks shared by the two appends; returns (arguments up to q_out, B, T, Hq, q_out)."""
+    if k.dim() != 3:
+        raise ValueError("k must be [T, Hkv, D]")
+    T = k.shape[0]
+    B = _check_map(block_table, cache_len, cu_seqlens, device)
+    if cu_seqlens is None and T != B:
+        raise ValueError("without cu_seqlens there is one token per sequence")
+    _check_rows(k, "k", T, Hkv, D, device)
+    _check_rows(v, "v", T, Hkv, D, device)
+    Hq, cos, sin, rope_len, rope_dim = 0, None, None, 0, 0
+    if rope is not None:
+        cos, sin = rope
+        if cos.dim() != 2 or 2 * cos.shape[1] > D:
+            raise ValueError("rope must be (cos, sin), each [positions, rotated elements / 2]")
+        _check_tensor(cos, "rope[0]", cos.shape, torch.float32, device)
+        _check_tensor(sin, "rope[1]", cos.shape, torch.float32, device)
+        rope_len, rope_dim = cos.shape[0], 2 * cos.shape[1]
+        if rope_dim < 16 or rope_dim % 16:
+            raise ValueError("the number of rotated elements must be a multiple of 16")
+    if q is not None:
+        if rope is None:
+            raise ValueError("q is only rotated: it needs rope")
+        if q.dim() != 3:
+            raise ValueError("q must be [T, Hq, D]")
+        Hq = q.shape[1]
+        _check_rows(q, "q", T, Hq, D, device)
+        _check_tensor(q_out, "q_out", (T, Hq, D), torch.bfloat16, device)
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=device)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    stride = lambda t: t.stride(0) if T > 1 else t.shape[1] * D  # noqa: E731
+    ptr = lambda t: None if t is None else t.data_ptr()          # noqa: E731
+    args = (ptr(q), k.data_ptr(), v.data_ptr(), 0 if q is None else stride(q), stride(k), stride(v),
+            ptr(cos), ptr(sin), rope_len, rope_dim)
+    return args, B, T, Hq, q_out
+
+
+def attn_append_kv(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                   block_table: torch.Tensor, cache_len: torch.Tensor,
+                   q: Optional[torch.Tensor] = None,
+                   rope: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                   interleaved: bool = False, cu_seqlens: Optional[torch.Tensor] = None,
+                   q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """Writes new tokens' keys and values into bf16 pages, rotating k (and q) on the way.
+
+    k, v [T, Hkv, D]: the new tokens, packed by cu_seqlens (int32 [B + 1]) or, without it, one
+    per sequence (T = B).  k_pages, v_pages [num_pages, page_size, Hkv, D], page_size 16 to 256
+    and a power of two.  block_table int32 [B, max_pages]; cache_len int32 [B] counts the cached
+    tokens with the new ones, so that new token i of n goes to position cache_len - n + i.
+    rope = (cos, sin), fp32 [positions, r / 2]: the first r elements of each head of k, and of
+    q [T, Hq, D] where it is given, are rotated by their position's row, pairing element j with
+    j + r / 2, or 2j with 2j + 1 if interleaved.  Returns the rotated q (q_out, which may be a
+    contiguous q itself), or None.
+
+    Tokens behind cu_seqlens[B], and tokens whose position is negative (an unused entry of the
+    batch has cache_len 0), are left out: nothing of them is written.  So are tokens past the
+    table or the rotation's positions, or whose page is not in the pool, and attn_device_status
+    then reports an invalid argument.  Two tokens that share a place leave either's value."""
+    P, Hkv, ps, D = _check_paged(k_pages, v_pages)
+    dev = k_pages.device
+    args, B, T, Hq, q_out = _append_args(k, v, block_table, cache_len, q, rope, cu_seqlens, q_out,
+                                         Hkv, D, dev)
+    _same_device(dev, v_pages)
+    if T:
+        capi.check(capi.attn_append_kv(
+            *args, interleaved, None if cu_seqlens is None else cu_seqlens.data_ptr(),
+            cache_len.data_ptr(), block_table.data_ptr(), None if q is None else q_out.data_ptr(),
+            k_pages.data_ptr(), v_pages.data_ptr(), B, T, Hq, Hkv, D, block_table.shape[1], P, ps,
+            _stream(dev)), "attn_append_kv")
+    return q_out
+
+
+def attn_append_kv4(k: torch.Tensor, v: torch.Tensor, pages: torch.Tensor,
+                    block_table: torch.Tensor, cache_len: torch.Tensor,
+                    q: Optional[torch.Tensor] = None,
+                    rope: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                    interleaved: bool = False, cu_seqlens: Optional[torch.Tensor] = None,
+                    q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """attn_append_kv into 4-bit pages (kv4_pages).  The bf16 values x that bf16 pages would hold
+    are kept per group of 64 elements as a minimum m, a step s = bf16((max - m) / 15) and codes
+    clamp(round((x - m) / s), 0, 15); a group with a NaN or an infinity reads back as NaN."""
+    P, Hkv, ps, D = _check_kv4(pages)
+    dev = pages.device
+    args, B, T, Hq, q_out = _append_args(k, v, block_table, cache_len, q, rope, cu_seqlens, q_out,
+                                         Hkv, D, dev)
+    if T:
+        capi.check(capi.attn_append_kv4(
+            *args, interleaved, None if cu_seqlens is None else cu_seqlens.data_ptr(),
+            cache_len.data_ptr(), block_table.data_ptr(), None if q is None else q_out.data_ptr(),
+            pages.data_ptr(), B, T, Hq, Hkv, D, block_table.shape[1], P, ps, _stream(dev)),
+            "attn_append_kv4")
+    return q_out
+
+
+def attn_gather_kv4(pages: torch.Tensor, block_table: torch.Tensor, cache_len: torch.Tensor,
+                    cu_seqlens: torch.Tensor, T: int, k: Optional[torch.Tensor] = None,
+                    v: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Cached tokens out of 4-bit pages, as packed bf16 k, v [T, Hkv, D] (the layout of attn_fwd):
+    the last n = cu_seqlens[b + 1] - cu_seqlens[b] tokens of sequence b, at positions
+    cache_len[b] - n ... (all of it for n = cache_len[b]; what attn_append_kv4 with the same
+    arrays has written).  A position that is negative or has no valid page reads as zeros (the
+    latter is reported as attn_append_kv does); rows behind cu_seqlens[B] are left as they were."""
+    P, Hkv, ps, D = _check_kv4(pages)
+    dev = pages.device
+    if cu_seqlens is None or T < 0:
+        raise ValueError("attn_gather_kv4 needs cu_seqlens and T >= 0")
+    B = _check_map(block_table, cache_len, cu_seqlens, dev)
+    _check_tensor(k, "k", (T, Hkv, D), torch.bfloat16, dev)
+    _check_tensor(v, "v", (T, Hkv, D), torch.bfloat16, dev)
+    k = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=dev) if k is None else k
+    v = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=dev) if v is None else v
+    if T:
+        capi.check(capi.attn_gather_kv4(
+            pages.data_ptr(), block_table.data_ptr(), cache_len.data_ptr(), cu_seqlens.data_ptr(),
+            k.data_ptr(), v.data_ptr(), B, T, Hkv, D, block_table.shape[1], P, ps, _stream(dev)),
+            "attn_gather_kv4")
+    return k, v
+
+
+def attn_decode_paged_workspace_size(q: torch.Tensor, k_pages: torch.Tensor,
+                                     block_table: torch.Tensor) -> int:
+    B, Hq, D = q.shape
+    return capi.attn_decode_paged_workspace_size(B, Hq, k_pages.shape[2], D, block_table.shape[1],
+                                                 k_pages.shape[1])
+
+
+def attn_decode_kv4_workspace_size(q: torch.Tensor, pages: torch.Tensor,
+                                   block_table: torch.Tensor) -> int:
+    B, Hq, D = q.shape
+    return capi.attn_decode_kv4_workspace_size(B, Hq, pages.shape[1], D, block_table.shape[1],
+                                               pages.shape[2] * KV4_UNIT)
+
+
+def _decode_args(q, D, block_table, cache_len, scale, out, lse, workspace, need, device):
+    """Checks and outputs shared by the two paged decodes."""
+    _check_inputs(q)
+    if q.dim() != 3 or q.shape[2] != D:
+        raise ValueError("q must be [B, Hq, D] with the cache's D")
+    B = _check_map(block_table, cache_len, None, device)
+    if q.shape[0] != B:
+        raise ValueError("q needs a row for each entry of cache_len")
+    _same_device(device, q)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    _check_tensor(out, "out", q.shape, torch.bfloat16, device)
+    _check_tensor(lse, "lse", q.shape[:2], torch.float32, device)
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=device) if lse is None else lse
+    if workspace is None:
+        workspace = torch.empty(max(need(), 1), dtype=torch.uint8, device=device)
+    return scale, out, lse, workspace, _workspace_bytes(workspace, device)
+
+
+def attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                      block_table: torch.Tensor, cache_len: torch.Tensor,
+                      scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                      lse: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """attn_decode over bf16 pages: q [B, Hq, D], k_pages and v_pages [num_pages, page_size, Hkv, D],
+    block_table int32 [B, max_pages], cache_len int32 [B].  Returns (o [B, Hq, D] bf16, lse
+    [B, Hq] fp32); a sequence of length 0 gets o = 0 and lse = -inf.  Table entries past a
+    sequence's length are not read; one within it that is not in the pool is reported by
+    attn_device_status and leaves that sequence's result unspecified."""
+    P, Hkv, ps, D = _check_paged(k_pages, v_pages)
+    dev = k_pages.device
+    _same_device(dev, v_pages)
+    scale, out, lse, workspace, nbytes = _decode_args(
+        q, D, block_table, cache_len, scale, out, lse, workspace,
+        lambda: attn_decode_paged_workspace_size(q, k_pages, block_table), dev)
+    B, Hq, _ = q.shape
+    capi.check(capi.attn_decode_paged(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+        cache_len.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, D, block_table.shape[1],
+        P, ps, scale, workspace.data_ptr(), nbytes, _stream(dev)), "attn_decode_paged")
+    return out, lse
+
+
+def attn_decode_kv4(q: torch.Tensor, pages: torch.Tensor, block_table: torch.Tensor,
+                    cache_len: torch.Tensor, scale: Optional[float] = None,
+                    out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """attn_decode_paged over 4-bit pages (kv4_pages, written by attn_append_kv4): the attention
+    of q over the values s * code + m that the pages stand for."""
+    P, Hkv, ps, D = _check_kv4(pages)
+    dev = pages.device
+    scale, out, lse, workspace, nbytes = _decode_args(
+        q, D, block_table, cache_len, scale, out, lse, workspace,
+        lambda: attn_decode_kv4_workspace_size(q, pages, block_table), dev)
+    B, Hq, _ = q.shape
+    capi.check(capi.attn_decode_kv4(
+        q.data_ptr(), pages.data_ptr(), block_table.data_ptr(), cache_len.data_ptr(),
+        out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, D, block_table.shape[1], P, ps, scale,
+        workspace.data_ptr(), nbytes, _stream(dev)), "attn_decode_kv4")
     return out, lse
 
 
