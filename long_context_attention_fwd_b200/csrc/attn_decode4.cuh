@@ -7,27 +7,29 @@
 // so the codes enter the products as small integers and the scales meet scores and weights, of
 // which there are 64 times fewer than codes.
 //
-// Bound by HBM when it is done right: 18 D bytes per 16 tokens and kv head for K and V together,
-// 3.6 times less than bf16.  At 24 bytes per clock and SM, turning codes into operands is the
-// larger part of the instructions, so each code is touched once, in registers, and never written
-// back to shared memory: the products are mma.sync m16n8k16 with the codes as the A operand
-// (16 tokens, or 16 elements of V, by 16) and the heads of a kv head as the 8-wide N side.  The
-// wide tensor-core path would need 4 times the bytes through shared memory for operands of which
-// a decode step uses 8 columns.
-//   K: codes become fp16 by OR-ing them into the mantissa of 1024 (exact), one subtraction (or
-//      fma for the upper nibble of a byte) leaves 0..15.  q is scaled by a power of two to fp16:
-//      exact but for 2^-25 of the row's largest element.  Sums are fp32.
+// Its floor is HBM: 18 D bytes per 16 tokens and kv head for K and V together, 3.6 times less
+// than bf16.  At the 24 bytes a clock that an SM gets, turning codes into operands is most of
+// the instructions, so each code is touched once, in registers, and never written back to shared
+// memory: the products are mma.sync m16n8k16 with the codes as the A operand (16 tokens, or 16
+// elements of V, by 16) and the heads of a kv head as the 8-wide N side.  tcgen05 would need the
+// operands as 16-bit values in shared or tensor memory, four times the bytes of the codes, for a
+// product of which a decode step uses 8 columns.
+//   A nibble needs no conversion: masked out of its word it is the fp16 subnormal code * 2^-24
+//   (or code * 2^-20, the upper nibble of a byte), which the tensor cores multiply exactly; one
+//   AND makes two operands.  The powers of two go into q (K) and into the final scale (V).
+//   K: q is scaled by a power of two to fp16, exact but for 2^-37 of the row's largest element.
 //   V: the words of two tokens are interleaved by byte permutes, so that the nibbles of a pair of
-//      tokens land in one register; codes become bf16 by OR-ing into 128, exact too.  The weights
-//      p s are rounded to bf16 (the steps are bf16 as well, and fp16 would not hold their range):
-//      a relative 2^-9 of each weight, on top of the output's own bf16 rounding.
+//      tokens land in one register.  The weights p s are rounded to fp16, a relative 2^-11 of
+//      each weight where bf16 would cost 2^-8.  fp16's range is kept by the softmax's reference
+//      R_h, which is not the largest score but moves so that p s, p = 2^(x - R), stays below 2^14
+//      and its largest value so far is at least 1; sums of p and of p m are fp32.
 //
-// Work: the tiles (32 tokens of one kv head) of all sequences form one line, cut into equal
+// Work: the tiles (kTile tokens of one kv head) of all sequences form one line, cut into equal
 // parts, one per block, whatever the lengths.  A block's warps take its tiles in turn; each has
-// its own ring of bulk copies (a unit of 16 tokens is one run of bytes) and its own running
-// maximum, sum and output.  At the end of a (sequence, kv head) the block's warps join theirs
-// through shared memory; where the pair is shared with other blocks, each writes its part and the
-// last one to finish joins them (done flags with the call's tag, as attn_decode_kernel does).
+// its own ring of bulk copies (a unit of 16 tokens is one run of bytes) and its own reference,
+// sum and output.  At the end of a (sequence, kv head) the block's warps join theirs through
+// shared memory; where the pair is shared with other blocks, each writes its part and the last
+// one to finish joins them (done flags with the call's tag, as attn_decode_kernel does).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -37,28 +39,31 @@
 namespace attn_sm100 {
 namespace decode4 {
 
-constexpr int kTileUnits = 2;
+constexpr int kTileUnits = 4;
 constexpr int kTile = kTileUnits * page::kUnit;  // tokens of a tile
-constexpr float kRescaleThreshold = 8.0f;        // weights stay below 2^8 of the running maximum
+constexpr uint32_t kTopWeight = 0x7400u;         // 2^14 as fp16: a weight this large moves the reference
+constexpr float kFirstWeight = 6.f;              // ... so that the largest becomes 2^6
+constexpr float kSmallStep = 9.313225746154785e-10f;  // 2^-30: smaller steps of V count as this in the reference
 
 enum : unsigned { kSiteFull = 0x520, kSiteDrain };
 
 // NT blocks of 8 heads per pass; a kv head with more than 8 query heads takes passes of 16.
 template <int D, int NT>
 struct Cfg {
-  static constexpr int W = NT == 1 ? 16 : 8;  // warps
+  static constexpr int W = 8;                 // warps
   static constexpr int NS = 2;                // ring stages of a warp
   static constexpr int THREADS = W * 32;
   static constexpr int HEADS = 8 * NT;
   static constexpr int TILE_BYTES = kTileUnits * page::Unit<D>::BYTES;
   static constexpr int OFF_RING = 0;
   static constexpr int OFF_O = OFF_RING + W * NS * TILE_BYTES;   // [W][HEADS][D] fp32
-  static constexpr int OFF_ML = OFF_O + W * HEADS * D * 4;       // [W][HEADS][2] fp32
-  static constexpr int OFF_BAR = OFF_ML + W * HEADS * 8;
-  static constexpr int OFF_MISC = OFF_BAR + W * NS * 8;          // 64 bytes
-  static constexpr int OFF_SCAN = OFF_MISC + 64;                 // [W] fp32/int scratch
-  static constexpr int SMEM_BYTES = OFF_SCAN + W * 4;
-  static_assert(TILE_BYTES % 16 == 0 && SMEM_BYTES <= 227 * 1024, "shared memory");
+  static constexpr int OFF_L = OFF_O + W * HEADS * D * 4;        // [W][HEADS] fp32
+  static constexpr int OFF_WT = OFF_L + W * HEADS * 4;           // [kMaxParts][HEADS] fp32
+  static constexpr int kMaxParts = 160;                          // blocks that can share an item
+  static constexpr int OFF_BAR = OFF_WT + kMaxParts * HEADS * 4;
+  static constexpr int OFF_MISC = OFF_BAR + W * NS * 8;          // abort flag per warp, merge flag
+  static constexpr int SMEM_BYTES = OFF_MISC + W * 4 + 16;
+  static_assert(TILE_BYTES % 16 == 0 && OFF_BAR % 8 == 0 && SMEM_BYTES <= 227 * 1024, "shared memory");
 };
 
 struct Params {
@@ -69,7 +74,7 @@ struct Params {
   int B, Hq, Hkv, G, RB;      // G query heads per kv head, in RB passes of HEADS
   int width, num_pages, log_ps;
   float* o_part;              // [2 * grid][HEADS][D]: a block's first and last shared part
-  float* ml_part;             // [2 * grid][HEADS][2]
+  float* l_part;              // [2 * grid][HEADS]
   unsigned long long* flags;  // [2 * grid]
   unsigned long long tag;
   __nv_bfloat16* o;           // [B][Hq][D]
@@ -80,62 +85,53 @@ struct Params {
 };
 
 // Token of a unit that row i (0..7) of the first product holds (row i + 8: 8 more).  The order
-// makes the four tokens that the second product reads at once fall into different banks.
+// spreads the four tokens that the second product reads at once over the banks.
 __device__ __forceinline__ int token_of(int i) { return i ^ ((i >> 1) & 1); }
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        const uint32_t (&b)[2]) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-}
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t y;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+  return y;
+}
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+__device__ __forceinline__ float step_of(uint32_t sm) { return __uint_as_float(sm << 16); }
+__device__ __forceinline__ float low_of(uint32_t sm) { return __uint_as_float(sm & 0xffff0000u); }
 
-// Codes at bits 0-3 and 16-19 (or 4-7 and 20-23) of w as an fp16 pair.
-__device__ __forceinline__ uint32_t f16_low(uint32_t w) {
-  const uint32_t x = (w & 0x000f000fu) | 0x64006400u;  // 1024 + code
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), __floats2half2_rn(1024.f, 1024.f));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t f16_high(uint32_t w) {
-  const uint32_t x = (w & 0x00f000f0u) | 0x64006400u;  // 1024 + 16 code
-  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&x), __floats2half2_rn(0.0625f, 0.0625f),
-                            __floats2half2_rn(-64.f, -64.f));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-// Codes at bits 0-3 and 16-19 of w as a bf16 pair.
-__device__ __forceinline__ uint32_t bf16_low(uint32_t w) {
-  const uint32_t x = (w & 0x000f000fu) | 0x43004300u;  // 128 + code
-  const __nv_bfloat162 r =
-      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), __floats2bfloat162_rn(128.f, 128.f));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
+constexpr uint32_t kLowNibbles = 0x000f000fu, kHighNibbles = 0x00f000f0u;
 
-__device__ __forceinline__ int tiles_of(const Params& p, int b) {
-  const int cap = p.width << p.log_ps;
-  const int L = min(max(__ldg(p.cache_len + b), 0), cap);
-  return (L + kTile - 1) / kTile;
+__device__ __forceinline__ int length_of(const Params& p, int b) {
+  return min(max(__ldg(p.cache_len + b), 0), p.width << p.log_ps);
 }
+__device__ __forceinline__ int tiles_of(int L) { return (L + kTile - 1) / kTile; }
 
 // Place on the line of tiles: tile j of the nt tiles of (sequence b, head block vh).
 struct Cursor {
-  int b, vh, j, nt;
+  int b, vh, j, nt, L;
   __device__ __forceinline__ void settle(const Params& p, int nv) {
     while (j >= nt) {
       j -= nt;
       if (++vh == nv) {
         vh = 0;
-        do ++b;
-        while (b < p.B && (nt = tiles_of(p, b)) == 0);
-        if (b >= p.B) return;  // past the end of the line
+        do {
+          if (++b >= p.B) return;  // past the end of the line
+          L = length_of(p, b);
+          nt = tiles_of(L);
+        } while (nt == 0);
       }
     }
   }
@@ -147,144 +143,139 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
   using U = page::Unit<D>;
   constexpr int NG = U::NG;
   constexpr int W = C::W;
+  constexpr int TU = kTileUnits;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = lane >> 2, c = lane & 3;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * C::NS;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
-  volatile int* s_merge = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-  volatile int* s_start = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);   // b, offset
-  int* s_scan = reinterpret_cast<int*>(smem + C::OFF_SCAN);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC) + warp;
+  volatile int* s_merge = reinterpret_cast<volatile int*>(smem + C::OFF_MISC) + W;
   float* s_o = reinterpret_cast<float*>(smem + C::OFF_O);
-  float* s_ml = reinterpret_cast<float*>(smem + C::OFF_ML);
+  float* s_l = reinterpret_cast<float*>(smem + C::OFF_L);
+  float* s_wt = reinterpret_cast<float*>(smem + C::OFF_WT);
   const int nv = p.Hkv * p.RB;
   const WaitCtl wc{p.status, abort_flag, p.timeout_ns};
 
-  if (tid == 0) *abort_flag = 0;
-  if (lane == 0)
+  if (lane == 0) {
+    *abort_flag = 0;
     for (int i = 0; i < C::NS; ++i) mbar_init(&full[i], 1);
-  fence_mbar_init();
+    fence_mbar_init();
+  }
+  __syncwarp();
 
-  // ---- this block's part [t0, t1) of the line, and where it starts
-  int total = 0;
-  for (int b = tid; b < p.B; b += C::THREADS) total += tiles_of(p, b);
-  total = __reduce_add_sync(0xffffffffu, total);
-  if (lane == 0) s_scan[warp] = total;
-  __syncthreads();
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) total += s_scan[w];
-  total *= nv;
-  const int chunk = max((total + int(gridDim.x) - 1) / int(gridDim.x), W);
+  // ---- this block's part [t0, t1) of the line, and where it starts (every warp by itself)
+  int total = 0, longest = 0;
+  for (int b = lane; b < p.B; b += 32) {
+    const int n = tiles_of(length_of(p, b));
+    total += n;
+    longest = max(longest, n);
+  }
+  total = __reduce_add_sync(0xffffffffu, total) * nv;
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  // Equal parts; while they are short, whole rounds of the warps, and no cut through sequences
+  // of at most two rounds: joining blocks costs more than a second round.
+  int chunk = (total + int(gridDim.x) - 1) / int(gridDim.x);
+  if (chunk < 4 * W) chunk = (chunk + W - 1) / W * W;
+  if (longest <= 2 * W) chunk = max(chunk, longest);
   const int t0 = min(total, int(blockIdx.x) * chunk), t1 = min(total, t0 + chunk);
-  __syncthreads();
 
   // Sequences without tokens: o = 0, lse = -inf.
   for (int b = blockIdx.x; b < p.B; b += gridDim.x)
-    if (tiles_of(p, b) == 0)
+    if (length_of(p, b) == 0)
       for (int i = tid; i < p.Hq * (D / 8); i += C::THREADS) {
         reinterpret_cast<uint4*>(p.o)[(long long)b * p.Hq * (D / 8) + i] = make_uint4(0u, 0u, 0u, 0u);
         if (i < p.Hq) p.lse[(long long)b * p.Hq + i] = -INFINITY;
       }
   if (t0 >= t1) return;
 
-  if (warp == 0) {
-    int before = 0;  // tiles (times nv) of the sequences before this group of 32
-    for (int b0 = 0;; b0 += 32) {
-      const int n = b0 + lane < p.B ? tiles_of(p, b0 + lane) * nv : 0;
-      int incl = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, before + incl > t0);
-      if (past) {
-        const int l = __ffs(past) - 1;
-        if (lane == l) {
-          s_start[0] = b0 + lane;
-          s_start[1] = t0 - (before + incl - n);
-        }
-        break;
-      }
-      before += __shfl_sync(0xffffffffu, incl, 31);
-    }
-  }
-  __syncthreads();
-
   Cursor item;  // the (sequence, head block) the block is at; j counts from the item's own start
-  item.b = s_start[0];
-  item.nt = tiles_of(p, item.b);
-  item.vh = s_start[1] / item.nt;
-  item.j = s_start[1] % item.nt;
+  for (int b0 = 0, before = 0;; b0 += 32) {
+    const int L = b0 + lane < p.B ? length_of(p, b0 + lane) : 0;
+    const int n = tiles_of(L) * nv;
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + incl > t0);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      const int off = t0 - before - __shfl_sync(0xffffffffu, incl - n, l);
+      item.b = b0 + l;
+      item.L = __shfl_sync(0xffffffffu, L, l);
+      item.nt = tiles_of(item.L);
+      item.vh = off / item.nt;
+      item.j = off % item.nt;
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
 
   // ---- this warp's copies: tiles t0 + warp, t0 + warp + W, ...
   uint8_t* ring = smem + C::OFF_RING + warp * C::NS * C::TILE_BYTES;
-  const int upp_log = p.log_ps - 4;          // units of a page
-  const int cap = p.width << p.log_ps;
+  const int upp_log = p.log_ps - 4;                  // units of a page
+  const int step_log = min(upp_log, 31 - __clz(TU)); // units of one copy
+  const long long page_bytes = ((long long)p.Hkv << upp_log) * U::BYTES;
   Cursor next = item;
   next.j += warp;
   next.settle(p, nv);
   int t_issue = t0 + warp;
   int pg_next = 0;
-  auto fetch_page = [&] {                     // lane i: page of unit i of the next tile
-    if (t_issue < t1 && lane < kTileUnits) {
-      const int u = next.j * kTileUnits + lane;
-      const int n = u >> upp_log;
-      pg_next = n < p.width ? __ldg(p.table + (long long)next.b * p.width + n) : 0;
-    }
+  const int lane_u = lane << step_log;               // first unit of this lane's copy
+  auto fetch_page = [&] {                            // page of this lane's copy of the next tile
+    const int u = next.j * TU + lane_u;
+    if (t_issue < t1 && lane_u < TU && u * page::kUnit < next.L)
+      pg_next = __ldg(p.table + (long long)next.b * p.width + (u >> upp_log));
   };
   auto issue = [&](int st) {
-    if (t_issue >= t1) return;
-    const int L = min(max(__ldg(p.cache_len + next.b), 0), cap);
-    const int units = min(kTileUnits, (L + page::kUnit - 1) / page::kUnit - next.j * kTileUnits);
+    const int units = min(TU, ((next.L + page::kUnit - 1) >> 4) - next.j * TU);
     if (lane == 0) mbar_arrive_expect_tx(&full[st], uint32_t(units) * U::BYTES);
     __syncwarp();
-    // One copy per page: a tile lies in one page, or its units in a page each.
-    const bool single = upp_log >= 1;
-    if (lane < (single ? 1 : units)) {
+    if (lane_u < units) {
       int pg = pg_next;
       if (pg < 0 || pg >= p.num_pages) {
         page::flag_bad_page(p.status, page::kSiteDecode4);
         pg = 0;
       }
-      const int u = next.j * kTileUnits + lane;
-      const uint8_t* src = p.pages + ((((long long)pg * p.Hkv + next.vh / p.RB) << upp_log) +
-                                      (u & ((1 << upp_log) - 1))) * U::BYTES;
-      bulk_load(ring + st * C::TILE_BYTES + lane * U::BYTES, src,
-                uint32_t(single ? units : 1) * U::BYTES, &full[st]);
+      const int g = p.RB == 1 ? next.vh : next.vh / p.RB;
+      const int u = (next.j * TU + lane_u) & ((1 << upp_log) - 1);
+      bulk_load(ring + st * C::TILE_BYTES + lane_u * U::BYTES,
+                p.pages + pg * page_bytes + ((g << upp_log) + u) * U::BYTES,
+                uint32_t(min(units - lane_u, 1 << step_log)) * U::BYTES, &full[st]);
     }
     t_issue += W;
     next.j += W;
-    if (t_issue < t1) next.settle(p, nv);
-    fetch_page();
+    if (t_issue < t1) {
+      next.settle(p, nv);
+      fetch_page();
+    }
   };
   fetch_page();
-  int issued = 0;
-  for (; issued < C::NS && t_issue < t1; ++issued) issue(issued);
+  for (int i = 0; i < C::NS && t_issue < t1; ++i) issue(i);
 
   // ---- tiles
-  int done = 0;      // tiles this warp has taken
-  int t = t0;        // start of the item on the line
+  int done = 0;             // tiles this warp has taken
+  int t = t0, tw = t0 + warp;  // start of the item's part on the line; this warp's next tile
   bool ok = true;
   const int key0 = token_of(r);
   while (t < t1) {
     const int e = min(t1, t + item.nt - item.j);         // end of the item's part
-    const int L = min(max(__ldg(p.cache_len + item.b), 0), cap);
-    const int g = item.vh / p.RB, rb = item.vh % p.RB;
+    const int L = item.L;
+    const int g = p.RB == 1 ? item.vh : item.vh / p.RB;
+    const int rb = item.vh - g * p.RB;
     const int h0 = g * p.G + rb * C::HEADS;              // first query head of the pass
     const int nh = min(C::HEADS, p.G - rb * C::HEADS);
-    const __nv_bfloat16* qrow = p.q + ((long long)item.b * p.Hq + h0) * D;
 
     uint32_t qf[NG][4][NT][2];
     float qsum[NG][NT][2], csc[NT][2];
-    float m_run[NT][2], l_run[NT][2], om[NG][NT][2];
+    float ref[NT][2], l_run[NT][2], om[NG][NT][2];
     float oacc[NG][4][NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e2 = 0; e2 < 2; ++e2) {
-        m_run[nt][e2] = -INFINITY;
+        ref[nt][e2] = -INFINITY;
         l_run[nt][e2] = 0.f;
 #pragma unroll
         for (int gg = 0; gg < NG; ++gg) om[gg][nt][e2] = 0.f;
@@ -298,8 +289,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
 #pragma unroll
           for (int k = 0; k < 4; ++k) oacc[gg][i][nt][k] = 0.f;
 
-    if (t0 + warp + done * W < e) {
+    if (tw < e) {
       // Queries of this warp's fragments: head nt * 8 + r, the elements of words 2c, 2c + 1.
+      const __nv_bfloat16* qrow = p.q + ((long long)item.b * p.Hq + h0) * D;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const bool have = nt * 8 + r < nh;
@@ -330,68 +322,77 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
 #pragma unroll
           for (int gg = 0; gg < NG; ++gg) sum[gg] += __shfl_xor_sync(0xffffffffu, sum[gg], o);
         }
-        // 2^-ex brings the row's largest element into [1, 2); both powers are normal numbers.
-        const int ex = min(max(int((__float_as_uint(big) >> 23) & 0xff) - 127, -126), 126);
-        const float down = __uint_as_float(uint32_t(127 - ex) << 23);
+        // down = 2^(13 - ex) brings the row's largest element into [2^13, 2^14); up = 2^ex.
+        const int ex = min(max(int((__float_as_uint(big) >> 23) & 0xff) - 127, -114), 127);
+        const float down = __uint_as_float(uint32_t(140 - ex) << 23);
         const float up = __uint_as_float(uint32_t(127 + ex) << 23);
 #pragma unroll
         for (int gg = 0; gg < NG; ++gg)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)   // step 2i + h of the group: elements 2h, 2h + 4 | 2h + 1, 2h + 5
+            for (int h = 0; h < 2; ++h)   // step 2i + h: elements 2h, 2h + 4 | 2h + 1, 2h + 5 of word i
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const __half2 y = __floats2half2_rn(x[gg][i][2 * h + k] * down, x[gg][i][2 * h + k + 4] * down);
-                qf[gg][2 * i + h][nt][k] = *reinterpret_cast<const uint32_t*>(&y);
-              }
-        // To the accumulator's layout: heads 2c and 2c + 1.
+              for (int k = 0; k < 2; ++k)  // k = 1: upper nibbles, 16 times too large
+                qf[gg][2 * i + h][nt][k] =
+                    pack_f16x2(x[gg][i][2 * h + k] * down * (k ? 0.0625f : 1.f),
+                               x[gg][i][2 * h + k + 4] * down * (k ? 0.0625f : 1.f));
+        // To the accumulator's layout: heads 2c and 2c + 1.  An accumulator holds
+        // 2^(13 - ex - 24) times the sum of q code.
 #pragma unroll
         for (int e2 = 0; e2 < 2; ++e2) {
           const int src = 4 * (2 * c + e2);
-          csc[nt][e2] = __shfl_sync(0xffffffffu, up, src) * p.scale_log2;
+          csc[nt][e2] = __shfl_sync(0xffffffffu, up, src) * p.scale_log2 * 2048.f;
           const float dn = __shfl_sync(0xffffffffu, down, src);
 #pragma unroll
-          for (int gg = 0; gg < NG; ++gg) qsum[gg][nt][e2] = __shfl_sync(0xffffffffu, sum[gg], src) * dn;
+          for (int gg = 0; gg < NG; ++gg)
+            qsum[gg][nt][e2] = __shfl_sync(0xffffffffu, sum[gg], src) * dn * 5.9604644775390625e-8f;
         }
       }
     }
 
-    for (; t0 + warp + done * W < e; ++done) {
+    for (bool first = true; tw < e; tw += W, ++done, first = false) {
       const int st = done % C::NS;
       ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[st], (done / C::NS) & 1, wc, kSiteFull));
       if (!ok) continue;
-      const uint8_t* tile = ring + st * C::TILE_BYTES;
-      const int key_base = (item.j + (t0 + warp + done * W - t)) * kTile;
-      const bool ragged = key_base + kTile > L;
-
-      // scores, times log2(e)
-      float sc[kTileUnits][NT][4];
+      uint8_t* tile = ring + st * C::TILE_BYTES;
+      const int left = L - (item.j + (tw - t)) * kTile;   // tokens from the tile's first on
+      if (left < kTile) {
+        // Behind the length lies anything: codes are harmless, scales are not.
+        for (int i = left + lane; i < kTile; i += 32) {
+          uint8_t* unit = tile + (i >> 4) * U::BYTES;
 #pragma unroll
-      for (int u = 0; u < kTileUnits; ++u) {
+          for (int gg = 0; gg < NG; ++gg) {
+            reinterpret_cast<uint32_t*>(unit + U::OFF_KS)[(i & 15) * NG + gg] = 0u;
+            reinterpret_cast<uint32_t*>(unit + U::OFF_VS)[(i & 15) * NG + gg] = 0u;
+          }
+        }
+        __syncwarp();
+      }
+
+      // scores x, times log2(e)
+      float x[TU][NT][4];
+#pragma unroll
+      for (int u = 0; u < TU; ++u) {
         const uint8_t* unit = tile + u * U::BYTES;
-        uint32_t w[2][2 * NG];   // [token half][2 * word + group]
+        uint32_t w[2][2 * NG];   // [token half][NG * word + group]
+        uint32_t sm[2][NG];
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           const uint8_t* src = unit + U::OFF_KC + (key0 + 8 * hh) * U::CODE + c * 8 * NG;
+          const uint8_t* ssrc = unit + U::OFF_KS + (key0 + 8 * hh) * U::SCALE;
           if constexpr (NG == 2) {
             const uint4 v = *reinterpret_cast<const uint4*>(src);
             w[hh][0] = v.x, w[hh][1] = v.y, w[hh][2] = v.z, w[hh][3] = v.w;
+            const uint2 y = *reinterpret_cast<const uint2*>(ssrc);
+            sm[hh][0] = y.x, sm[hh][1] = y.y;
           } else {
             const uint2 v = *reinterpret_cast<const uint2*>(src);
             w[hh][0] = v.x, w[hh][1] = v.y;
+            sm[hh][0] = *reinterpret_cast<const uint32_t*>(ssrc);
           }
         }
-        uint32_t sm[2][NG];
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-          for (int gg = 0; gg < NG; ++gg)
-            sm[hh][gg] = *reinterpret_cast<const uint32_t*>(unit + U::OFF_KS + (key0 + 8 * hh) * U::SCALE + 4 * gg);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) sc[u][nt][k] = 0.f;
+        float sc[NT][4];
 #pragma unroll
         for (int gg = 0; gg < NG; ++gg) {
           float acc[NT][4];
@@ -402,64 +403,96 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t x0 = w[0][NG * i + gg], x1 = w[1][NG * i + gg];
-            const uint32_t a0[4] = {f16_low(x0), f16_low(x1), f16_high(x0), f16_high(x1)};
             const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
-            const uint32_t a1[4] = {f16_low(y0), f16_low(y1), f16_high(y0), f16_high(y1)};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma_f16(acc[nt], a0, qf[gg][2 * i][nt]);
-              mma_f16(acc[nt], a1, qf[gg][2 * i + 1][nt]);
+              mma_f16(acc[nt], x0 & kLowNibbles, x1 & kLowNibbles, x0 & kHighNibbles, x1 & kHighNibbles, qf[gg][2 * i][nt]);
+              mma_f16(acc[nt], y0 & kLowNibbles, y1 & kLowNibbles, y0 & kHighNibbles, y1 & kHighNibbles, qf[gg][2 * i + 1][nt]);
             }
           }
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const float s = __uint_as_float(sm[hh][gg] << 16), m = __uint_as_float(sm[hh][gg] & 0xffff0000u);
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e2 = 0; e2 < 2; ++e2)
-                sc[u][nt][2 * hh + e2] = fmaf(s, acc[nt][2 * hh + e2], fmaf(m, qsum[gg][nt][e2], sc[u][nt][2 * hh + e2]));
-          }
+            for (int k = 0; k < 4; ++k) {
+              const float s = step_of(sm[k >> 1][gg]), m = low_of(sm[k >> 1][gg]);
+              const float y = m * qsum[gg][nt][k & 1];
+              sc[nt][k] = gg == 0 ? fmaf(s, acc[nt][k], y) : sc[nt][k] + fmaf(s, acc[nt][k], y);
+            }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) sc[u][nt][k] *= csc[nt][k & 1];
+          for (int k = 0; k < 4; ++k) x[u][nt][k] = sc[nt][k] * csc[nt][k & 1];
       }
-      if (ragged) {
+      if (left < kTile) {
 #pragma unroll
-        for (int u = 0; u < kTileUnits; ++u)
+        for (int u = 0; u < TU; ++u)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (key_base + u * page::kUnit + key0 + 8 * (k >> 1) >= L) sc[u][nt][k] = -INFINITY;
+              if (u * page::kUnit + key0 + 8 * (k >> 1) >= left) x[u][nt][k] = -INFINITY;
       }
 
-      // running maximum: moved only when a weight would pass 2^kRescaleThreshold
-      bool need = false;
-      float mx[NT][2];
+      // weights p s in fp16; the reference moves when one reaches 2^14 (and on the first tile)
+      uint32_t vs[TU][2][NG];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int u = 0; u < TU; ++u)
 #pragma unroll
-        for (int e2 = 0; e2 < 2; ++e2) {
-          float x = fmaxf(sc[0][nt][e2], sc[0][nt][2 + e2]);
-#pragma unroll
-          for (int u = 1; u < kTileUnits; ++u) x = fmax3(x, sc[u][nt][e2], sc[u][nt][2 + e2]);
-          mx[nt][e2] = x;
-          need = need || x > m_run[nt][e2] + kRescaleThreshold;
+        for (int hh = 0; hh < 2; ++hh) {
+          const uint8_t* ssrc = tile + u * U::BYTES + U::OFF_VS + (key0 + 8 * hh) * U::SCALE;
+          if constexpr (NG == 2) {
+            const uint2 y = *reinterpret_cast<const uint2*>(ssrc);
+            vs[u][hh][0] = y.x, vs[u][hh][1] = y.y;
+          } else {
+            vs[u][hh][0] = *reinterpret_cast<const uint32_t*>(ssrc);
+          }
         }
-      if (__any_sync(0xffffffffu, need)) {
+      uint32_t pw[TU][NG][NT][2];
+      float pr[TU][NT][4];
+      auto weigh = [&]() -> bool {
+        uint32_t top = 0u;
+#pragma unroll
+        for (int u = 0; u < TU; ++u)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              const float p0 = ex2_approx(x[u][nt][2 * hh] - ref[nt][0]);
+              const float p1 = ex2_approx(x[u][nt][2 * hh + 1] - ref[nt][1]);
+              pr[u][nt][2 * hh] = p0;
+              pr[u][nt][2 * hh + 1] = p1;
+#pragma unroll
+              for (int gg = 0; gg < NG; ++gg) {
+                const float s = step_of(vs[u][hh][gg]);
+                pw[u][gg][nt][hh] = pack_f16x2(p0 * s, p1 * s);
+                top = max_f16x2(top, pw[u][gg][nt][hh]);
+              }
+            }
+        return (top & 0xffffu) >= kTopWeight || (top >> 16) >= kTopWeight;
+      };
+      bool move = first;
+      if (!first) move = __any_sync(0xffffffffu, weigh());
+      if (move) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e2 = 0; e2 < 2; ++e2) {
-            float x = mx[nt][e2];
+            float y = -INFINITY;
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-            const float m_new = fmaxf(m_run[nt][e2], x);
-            const float alpha = m_new == -INFINITY ? 1.f : ex2_approx(m_run[nt][e2] - m_new);
-            m_run[nt][e2] = m_new;
+            for (int u = 0; u < TU; ++u)
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                float s = fmaxf(step_of(vs[u][hh][0]), kSmallStep);
+                if constexpr (NG == 2) s = fmaxf(s, step_of(vs[u][hh][1]));
+                y = fmaxf(y, x[u][nt][2 * hh + e2] + __log2f(s));
+              }
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+            const float was = ref[nt][e2];
+            y = fmaxf(was, y - kFirstWeight);
+            const float alpha = first ? 0.f : ex2_approx(was - y);
+            ref[nt][e2] = y == -INFINITY ? 0.f : y;
             l_run[nt][e2] *= alpha;
 #pragma unroll
             for (int gg = 0; gg < NG; ++gg) {
@@ -471,24 +504,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
               }
             }
           }
+        weigh();
       }
 
-      // weights and the second product
-      float mneg[NT][2];
+      // sums and the second product
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e2 = 0; e2 < 2; ++e2) mneg[nt][e2] = m_run[nt][e2] == -INFINITY ? 0.f : m_run[nt][e2];
-#pragma unroll
-      for (int u = 0; u < kTileUnits; ++u) {
+      for (int u = 0; u < TU; ++u) {
         const uint8_t* unit = tile + u * U::BYTES;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            sc[u][nt][k] = ex2_approx(sc[u][nt][k] - mneg[nt][k & 1]);
-            l_run[nt][k & 1] += sc[u][nt][k];
-          }
         uint32_t wv[4][NG];   // tokens of pair slots 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -501,37 +523,39 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
           }
         }
 #pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) l_run[nt][k & 1] += pr[u][nt][k];
+#pragma unroll
         for (int gg = 0; gg < NG; ++gg) {
           uint32_t pb[NT][2];
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            uint32_t sm = *reinterpret_cast<const uint32_t*>(unit + U::OFF_VS + (key0 + 8 * hh) * U::SCALE + 4 * gg);
-            if (ragged && key_base + u * page::kUnit + key0 + 8 * hh >= L) sm = 0u;  // whatever lies there
-            const float s = __uint_as_float(sm << 16), m = __uint_as_float(sm & 0xffff0000u);
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              const float m = low_of(vs[u][hh][gg]);
+              om[gg][nt][0] = fmaf(pr[u][nt][2 * hh], m, om[gg][nt][0]);
+              om[gg][nt][1] = fmaf(pr[u][nt][2 * hh + 1], m, om[gg][nt][1]);
+              pb[nt][hh] = transpose8x8(pw[u][gg][nt][hh]);
+            }
+          uint32_t a = __byte_perm(wv[0][gg], wv[1][gg], 0x5410), b = __byte_perm(wv[0][gg], wv[1][gg], 0x7632);
+          uint32_t cc = __byte_perm(wv[2][gg], wv[3][gg], 0x5410), d = __byte_perm(wv[2][gg], wv[3][gg], 0x7632);
+#pragma unroll
+          for (int i = 0; i < 4; i += 2) {   // rows r: element i of the word; rows r + 8: element i + 4
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const float p0 = sc[u][nt][2 * hh], p1 = sc[u][nt][2 * hh + 1];
-              om[gg][nt][0] = fmaf(p0, m, om[gg][nt][0]);
-              om[gg][nt][1] = fmaf(p1, m, om[gg][nt][1]);
-              pb[nt][hh] = transpose8x8(pack_bf16x2(p0 * s, p1 * s));
+              mma_f16(oacc[gg][i][nt], a & kLowNibbles, b & kLowNibbles, cc & kLowNibbles, d & kLowNibbles, pb[nt]);
+              mma_f16(oacc[gg][i + 1][nt], a & kHighNibbles, b & kHighNibbles, cc & kHighNibbles, d & kHighNibbles, pb[nt]);
             }
-          }
-          const uint32_t ab_lo = __byte_perm(wv[0][gg], wv[1][gg], 0x5410), ab_hi = __byte_perm(wv[0][gg], wv[1][gg], 0x7632);
-          const uint32_t cd_lo = __byte_perm(wv[2][gg], wv[3][gg], 0x5410), cd_hi = __byte_perm(wv[2][gg], wv[3][gg], 0x7632);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {   // rows r: element i of the word; rows r + 8: element i + 4
-            const uint32_t a[4] = {bf16_low(ab_lo >> (4 * i)), bf16_low(ab_hi >> (4 * i)),
-                                   bf16_low(cd_lo >> (4 * i)), bf16_low(cd_hi >> (4 * i))};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_bf16(oacc[gg][i][nt], a, pb[nt]);
+            a >>= 8, b >>= 8, cc >>= 8, d >>= 8;
           }
         }
       }
       __syncwarp();  // every lane has read the stage
-      issue(st);
+      if (t_issue < t1) issue(st);
     }
 
-    // ---- join the warps' parts of this item
+    // ---- join the warps' parts of this item: normalised outputs, log2 sums
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -544,18 +568,18 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
         }
         const int h = nt * 8 + 2 * c + e2;
         if (h < nh) {
-          if (r == 0) {
-            s_ml[(warp * C::HEADS + h) * 2] = m_run[nt][e2];
-            s_ml[(warp * C::HEADS + h) * 2 + 1] = l_run[nt][e2];
-          }
+          const float l = l_run[nt][e2];
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          if (r == 0) s_l[warp * C::HEADS + h] = l == 0.f ? -INFINITY : ref[nt][e2] + log2f(l);
 #pragma unroll
           for (int gg = 0; gg < NG; ++gg) {
-            const float add = om[gg][nt][e2];
+            const float add = om[gg][nt][e2] * inv;
+            const float lo = inv * 16777216.f, hi = inv * 1048576.f;   // undo the subnormals' 2^-24, 2^-20
             float4* dst = reinterpret_cast<float4*>(s_o + (warp * C::HEADS + h) * D + gg * 64 + r * 8);
-            dst[0] = make_float4(oacc[gg][0][nt][e2] + add, oacc[gg][1][nt][e2] + add,
-                                 oacc[gg][2][nt][e2] + add, oacc[gg][3][nt][e2] + add);
-            dst[1] = make_float4(oacc[gg][0][nt][2 + e2] + add, oacc[gg][1][nt][2 + e2] + add,
-                                 oacc[gg][2][nt][2 + e2] + add, oacc[gg][3][nt][2 + e2] + add);
+            dst[0] = make_float4(fmaf(oacc[gg][0][nt][e2], lo, add), fmaf(oacc[gg][1][nt][e2], hi, add),
+                                 fmaf(oacc[gg][2][nt][e2], lo, add), fmaf(oacc[gg][3][nt][e2], hi, add));
+            dst[1] = make_float4(fmaf(oacc[gg][0][nt][2 + e2], lo, add), fmaf(oacc[gg][1][nt][2 + e2], hi, add),
+                                 fmaf(oacc[gg][2][nt][2 + e2], lo, add), fmaf(oacc[gg][3][nt][2 + e2], hi, add));
           }
         }
       }
@@ -563,37 +587,38 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
     const int a_line = t - item.j, e_line = a_line + item.nt;   // the whole item on the line
     const bool shared_item = a_line < t0 || e_line > t1;
     const int slot = 2 * blockIdx.x + (a_line < t0 ? 0 : 1);
+    const long long row0 = (long long)item.b * p.Hq + h0;
+    const int nw = min(W, e - t);                               // warps that had a tile
+    const int w0 = (t - t0) % W;                                // the first of them
     for (int i = tid; i < nh * (D / 4); i += C::THREADS) {
       const int h = i / (D / 4), d4 = i % (D / 4);
       float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < W; ++w) M = fmaxf(M, s_ml[(w * C::HEADS + h) * 2]);
+      for (int k = 0; k < nw; ++k) M = fmaxf(M, s_l[((w0 + k) % W) * C::HEADS + h]);
       const float Mz = M == -INFINITY ? 0.f : M;
       float l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int w = 0; w < W; ++w) {
-        const float x = ex2_approx(s_ml[(w * C::HEADS + h) * 2] - Mz);
-        const float4 y = reinterpret_cast<const float4*>(s_o)[(w * C::HEADS + h) * (D / 4) + d4];
-        l = fmaf(x, s_ml[(w * C::HEADS + h) * 2 + 1], l);
-        o.x = fmaf(x, y.x, o.x), o.y = fmaf(x, y.y, o.y), o.z = fmaf(x, y.z, o.z), o.w = fmaf(x, y.w, o.w);
+      for (int k = 0; k < nw; ++k) {
+        const int w = (w0 + k) % W;
+        const float y = ex2_approx(s_l[w * C::HEADS + h] - Mz);
+        const float4 v = reinterpret_cast<const float4*>(s_o)[(w * C::HEADS + h) * (D / 4) + d4];
+        l += y;
+        o.x = fmaf(y, v.x, o.x), o.y = fmaf(y, v.y, o.y), o.z = fmaf(y, v.z, o.z), o.w = fmaf(y, v.w, o.w);
       }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+      const float lse2 = l == 0.f ? -INFINITY : M + log2f(l);
       if (shared_item) {
         reinterpret_cast<float4*>(p.o_part)[((long long)slot * C::HEADS + h) * (D / 4) + d4] = o;
-        if (d4 == 0) {
-          p.ml_part[((long long)slot * C::HEADS + h) * 2] = M;
-          p.ml_part[((long long)slot * C::HEADS + h) * 2 + 1] = l;
-        }
+        if (d4 == 0) p.l_part[(long long)slot * C::HEADS + h] = lse2;
       } else {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const long long row = (long long)item.b * p.Hq + h0 + h;
-        reinterpret_cast<uint2*>(p.o)[row * (D / 4) + d4] =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (d4 == 0) p.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994530942f;
+        reinterpret_cast<uint2*>(p.o)[(row0 + h) * (D / 4) + d4] = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+        if (d4 == 0) p.lse[row0 + h] = lse2 * 0.69314718055994530942f;
       }
     }
     if (shared_item) {
       const int c0 = a_line / chunk, c1 = (e_line - 1) / chunk;   // the blocks that share the item
+      // A block's slot: its first, unless the item begins in its part.
+      auto slot_of = [&](int k) { return 2 * k + (a_line < k * chunk ? 0 : 1); };
       __threadfence();
       __syncthreads();
       if (warp == 0) {
@@ -601,8 +626,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
         if (lane == 0) fl[slot] = p.tag;
         __syncwarp();
         __threadfence();
-        // Block c0 started the item (unless it began exactly at its part: still its last slot).
-        auto slot_of = [&](int k) { return 2 * k + (a_line < k * chunk ? 0 : 1); };
         bool all = true;
         for (int k = c0 + lane; k <= c1; k += 32) all = all && fl[slot_of(k)] == p.tag;
         all = __all_sync(0xffffffffu, all);
@@ -613,28 +636,39 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
       __syncthreads();
       if (*s_merge) {
         __threadfence();
+        const int parts = c1 - c0 + 1;
+        for (int h = warp; h < nh; h += W) {   // the parts' weights, a warp per head
+          float M = -INFINITY, l = 0.f;
+          for (int k = lane; k < parts; k += 32) M = fmaxf(M, __ldcg(p.l_part + (long long)slot_of(c0 + k) * C::HEADS + h));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+          const float Mz = M == -INFINITY ? 0.f : M;
+          for (int k = lane; k < parts; k += 32) {
+            const float y = ex2_approx(__ldcg(p.l_part + (long long)slot_of(c0 + k) * C::HEADS + h) - Mz);
+            s_wt[k * C::HEADS + h] = y;
+            l += y;
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+          if (lane == 0) {
+            s_l[h] = l == 0.f ? 0.f : 1.f / l;
+            p.lse[row0 + h] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994530942f;
+          }
+        }
+        __syncthreads();
         for (int i = tid; i < nh * (D / 4); i += C::THREADS) {
           const int h = i / (D / 4), d4 = i % (D / 4);
-          float M = -INFINITY, l = 0.f;
           float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int k = c0; k <= c1; ++k) {
-            const long long s = 2 * k + (a_line < k * chunk ? 0 : 1);
-            M = fmaxf(M, __ldcg(p.ml_part + (s * C::HEADS + h) * 2));
+#pragma unroll 8
+          for (int k = 0; k < parts; ++k) {
+            const float y = s_wt[k * C::HEADS + h];
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.o_part) +
+                                    ((long long)slot_of(c0 + k) * C::HEADS + h) * (D / 4) + d4);
+            o.x = fmaf(y, v.x, o.x), o.y = fmaf(y, v.y, o.y), o.z = fmaf(y, v.z, o.z), o.w = fmaf(y, v.w, o.w);
           }
-          const float Mz = M == -INFINITY ? 0.f : M;
-#pragma unroll 4
-          for (int k = c0; k <= c1; ++k) {
-            const long long s = 2 * k + (a_line < k * chunk ? 0 : 1);
-            const float x = ex2_approx(__ldcg(p.ml_part + (s * C::HEADS + h) * 2) - Mz);
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(p.o_part) + (s * C::HEADS + h) * (D / 4) + d4);
-            l = fmaf(x, __ldcg(p.ml_part + (s * C::HEADS + h) * 2 + 1), l);
-            o.x = fmaf(x, y.x, o.x), o.y = fmaf(x, y.y, o.y), o.z = fmaf(x, y.z, o.z), o.w = fmaf(x, y.w, o.w);
-          }
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          const long long row = (long long)item.b * p.Hq + h0 + h;
-          reinterpret_cast<uint2*>(p.o)[row * (D / 4) + d4] =
+          const float inv = s_l[h];
+          reinterpret_cast<uint2*>(p.o)[(row0 + h) * (D / 4) + d4] =
               make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-          if (d4 == 0) p.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994530942f;
         }
       }
     }

@@ -482,7 +482,7 @@ unsigned grid_of(long long need, unsigned most) { return unsigned(need < most ? 
 // tile for every warp.  Up to 8 query heads of a kv head take one pass of 8, more take passes
 // of 16.  The workspace holds two shared parts per block.
 struct Decode4Ws {
-  size_t ml_part, flags, total;
+  size_t l_part, flags, total;
   long long tiles;
   int nt, passes;
   unsigned grid;
@@ -492,13 +492,15 @@ Decode4Ws decode4_ws(int B, int Hq, int Hkv, int D, int Lmax) {
   const int G = Hq / Hkv;
   w.nt = G <= 8 ? 1 : 2;
   const int heads = 8 * w.nt;
-  const int warps = w.nt == 1 ? decode4::Cfg<128, 1>::W : decode4::Cfg<128, 2>::W;
+  constexpr int warps = decode4::Cfg<128, 1>::W;
+  static_assert(warps == decode4::Cfg<128, 2>::W, "one plan for both");
+  static_assert(kPlanSMs <= decode4::Cfg<128, 1>::kMaxParts, "blocks that can share an item");
   w.passes = (G + heads - 1) / heads;
   w.tiles = (long long)((Lmax + decode4::kTile - 1) / decode4::kTile) * B * Hkv * w.passes;
   w.grid = grid_of((w.tiles + warps - 1) / warps, kPlanSMs);
   const size_t parts = 2 * size_t(w.grid) * heads;
-  w.ml_part = round_up(parts * D * sizeof(float), 256);
-  w.flags = w.ml_part + round_up(parts * 2 * sizeof(float), 256);
+  w.l_part = round_up(parts * D * sizeof(float), 256);
+  w.flags = w.l_part + round_up(parts * sizeof(float), 256);
   w.total = w.flags + round_up(2 * size_t(w.grid) * 8, 256);
   return w;
 }
@@ -877,7 +879,7 @@ attn_status attn_decode_kv4(const void* q, const void* pages, const int32_t* blo
   p.num_pages = num_pages;
   p.log_ps = log_ps;
   p.o_part = reinterpret_cast<float*>(ws);
-  p.ml_part = reinterpret_cast<float*>(ws + w.ml_part);
+  p.l_part = reinterpret_cast<float*>(ws + w.l_part);
   p.flags = reinterpret_cast<unsigned long long*>(ws + w.flags);
   p.tag = next_decode_tag();
   p.o = static_cast<__nv_bfloat16*>(o);
