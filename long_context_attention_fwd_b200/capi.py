@@ -7,6 +7,7 @@ is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 import threading
@@ -96,6 +97,8 @@ def declared_symbols() -> list:
 def lib():
     """The loaded library (built on first use if nvcc is available)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -200,6 +203,7 @@ def attn_gather_kv4(pages, block_table, cache_len, cu_seqlens, k, v, B, T, Hkv, 
                                  max_pages, num_pages, page_size, stream)
 
 
+@functools.lru_cache(maxsize=1024)
 def attn_decode_paged_workspace_size(B, Hq, Hkv, D, max_pages, page_size) -> int:
     return lib().attn_decode_paged_workspace_size(B, Hq, Hkv, D, max_pages, page_size)
 
@@ -211,6 +215,7 @@ def attn_decode_paged(q, k_pages, v_pages, block_table, cache_len, o, lse, B, Hq
                                    workspace_bytes, stream)
 
 
+@functools.lru_cache(maxsize=1024)
 def attn_decode_kv4_workspace_size(B, Hq, Hkv, D, max_pages, page_size) -> int:
     return lib().attn_decode_kv4_workspace_size(B, Hq, Hkv, D, max_pages, page_size)
 

@@ -6,15 +6,18 @@
 // with (a, b) = (x[j], x[j + half]) or, interleaved, (x[2j], x[2j + 1]), and writes k and v where
 // the page table says: as bf16, or as 4-bit codes with a step and a minimum per 64 elements,
 //     m = min x,  s = bf16((max x - m) / 15),  code = rint((x - m) / s) in 0..15,
-// of the bf16 values x.  The divisions are IEEE fp32: x - m and s have so few bits that the
-// rounded quotient is on the right side of every half, so the codes are those of exact arithmetic.
+// of the bf16 values x.  The quotient is rounded as in exact arithmetic: a product with 1 / s
+// gives a candidate, and the remainder x - m - code s, which fp32 holds exactly, corrects it.
+// (IEEE divisions, 16 a thread, took the 4-bit append three times as long as the bf16 one.)
 // A group with a NaN or an infinity, or whose range leaves fp32, gets s = m = NaN and reads back
 // as NaN.
 //
-// Bound by HBM: every input element is read once and every output written once.  One block takes
-// a token: D / 16 threads hold a row in two 16-byte chunks, chosen so that rotation partners meet
-// in one thread, and a thread's angles serve every head of the token.  The data loads do not wait
-// for the page table.
+// Bound by HBM: every input element is read once and every output written once.  D / 16 threads
+// hold a row in two 16-byte chunks, chosen so that rotation partners meet in one thread, and a
+// thread's angles serve every head of the token.  A warp takes a token, or a share of its rows
+// where there are fewer tokens than warps to fill the SMs; it has kAhead rows' loads in flight,
+// and the first of them do not wait for the page table.  (A block per token: 152 us for 30K
+// tokens of 28 + 2 x 4 heads where a warp per token takes 100.)
 #pragma once
 #include <cuda_bf16.h>
 
@@ -24,7 +27,7 @@ namespace attn_sm100 {
 namespace append {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 2;  // rows a thread loads before it waits for the token's place
+constexpr int kAhead = 3;  // rows a thread has in flight
 
 struct Params {
   page::PageMap map;
@@ -36,6 +39,7 @@ struct Params {
   const float* sin;
   int rope_len, half, interleaved;
   int nq, Hkv;              // query heads written (0 without q), kv heads
+  int share_log;            // 2^share_log warps share a token
   __nv_bfloat16* q_out;     // [T][nq][D]
   __nv_bfloat16* k_pages;   // bf16 pages
   __nv_bfloat16* v_pages;
@@ -82,13 +86,28 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-// Eight codes of one word.
+// Eight codes of one word: round((x - m) / s), ties to even, in 0..15.
 __device__ __forceinline__ uint32_t encode(const Chunk& c, float m, float s) {
   uint32_t w = 0;
+  if (s < 1e-36f) {  // 1 / s may leave fp32; s = 0: equal elements, or a group that is not finite
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float t = s > 0.f ? rintf(__fdiv_rn(__fsub_rn(c.x[j], m), s)) : 0.f;
+      w |= uint32_t(fminf(t, 15.f)) << (4 * j);
+    }
+    return w;
+  }
+  const float inv = __frcp_rn(s), half = 0.5f * s;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float t = s > 0.f ? rintf(__fdiv_rn(__fsub_rn(c.x[j], m), s)) : 0.f;
-    w |= uint32_t(fminf(t, 15.f)) << (4 * j);  // t >= 0: m is the group's minimum
+    const float a = __fsub_rn(c.x[j], m);        // >= 0: m is the group's minimum
+    const float t = fminf(rintf(a * inv), 15.f);
+    const float rem = fmaf(-t, s, a);            // exact: t s has 12 bits, and a is near it
+    int q = int(t);
+    const bool odd = q & 1;
+    if (rem > half || (rem == half && odd)) ++q;
+    if (rem < -half || (rem == -half && odd)) --q;
+    w |= uint32_t(min(q, 15)) << (4 * j);
   }
   return w;
 }
@@ -96,9 +115,9 @@ __device__ __forceinline__ uint32_t encode(const Chunk& c, float m, float s) {
 template <int D, bool KV4>
 __global__ void __launch_bounds__(kThreads) append_kernel(const Params p) {
   constexpr int TPR = D / 16;            // threads of a row
-  constexpr int RPP = kThreads / TPR;    // rows of a pass
-  const int tr = threadIdx.x % TPR;
-  const int r0 = threadIdx.x / TPR;
+  constexpr int RPP = 32 / TPR;          // rows of a warp's pass
+  const int lane = threadIdx.x & 31;
+  const int tr = lane % TPR;
   const int rows = p.nq + 2 * p.Hkv;     // a token's rows: q heads, k heads, v heads
   const int hc = p.half / 8;
   const bool turned = tr < hc;
@@ -114,17 +133,24 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Params p) {
     u[1] = reinterpret_cast<const uint4*>(src)[cb];
   };
 
-  for (int t = blockIdx.x; t < p.map.T; t += gridDim.x) {
+  const long long items = (long long)p.map.T << p.share_log;
+  const long long nwarp = (long long)gridDim.x * (kThreads / 32);
+  const int stride = RPP << p.share_log;  // rows from one pass to the next
+  for (long long item = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); item < items; item += nwarp) {
+    const int t = int(item >> p.share_log);
+    const int first = (int(item) & ((1 << p.share_log) - 1)) * RPP;   // the warp's first row
+    const int r0 = first + lane / TPR;
+    if (first >= rows) continue;
     uint4 u[kAhead][2];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
-      if (r0 + i * RPP < rows) load(t, r0 + i * RPP, u[i]);
+      if (r0 + i * stride < rows) load(t, r0 + i * stride, u[i]);
 
     int pos, pg, slot;
     page::Placed st = page::place_token(p.map, t, pos, pg, slot);
     if (st == page::kFound && p.half > 0 && pos >= p.rope_len) st = page::kBad;
-    if (st == page::kBad && threadIdx.x == 0) page::flag_bad_page(p.status, page::kSiteAppend);
-    if (st != page::kFound) continue;  // the same in every thread of the block
+    if (st == page::kBad && lane == 0) page::flag_bad_page(p.status, page::kSiteAppend);
+    if (st != page::kFound) continue;  // the same in every lane
 
     float c[8], s[8];
     if (turned) {
@@ -136,12 +162,16 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Params p) {
       *reinterpret_cast<float4*>(s + 4) = __ldg(reinterpret_cast<const float4*>(p.sin + at) + 1);
     }
 
-    for (int base = 0; base < rows; base += kAhead * RPP) {
+    for (int base = 0; first + base < rows; base += kAhead * stride) {
+      if (base > 0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+          if (r0 + base + i * stride < rows) load(t, r0 + base + i * stride, u[i]);
+      }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const int row = base + i * RPP + r0;
+        const int row = base + i * stride + r0;
         const bool live = row < rows;
-        if (base > 0 && live) load(t, row, u[i]);
         if (!__any_sync(0xffffffffu, live)) continue;
         if (live && turned && row < p.nq + p.Hkv) {
           Chunk a = unpack(u[i][0]), b = unpack(u[i][1]);
@@ -217,8 +247,13 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Params p) {
             uint8_t* unit = p.pages + ((((long long)pg * p.Hkv + h) << upp_log) + (slot >> 4)) * U::BYTES;
             const int j = slot & 15;
             uint32_t* code = reinterpret_cast<uint32_t*>(unit + (is_v ? U::OFF_VC : U::OFF_KC) + j * U::CODE);
-            code[U::NG * (ca & 7) + ga] = encode(a, la, sa);
-            code[U::NG * (cb & 7) + gb] = encode(b, lb, sb);
+            const uint32_t wa = encode(a, la, sa), wb = encode(b, lb, sb);
+            if (U::NG == 2 && cb == ca + 8) {   // the same word of both groups: neighbours
+              *reinterpret_cast<uint2*>(code + 2 * ca) = make_uint2(wa, wb);
+            } else {
+              code[U::NG * (ca & 7) + ga] = wa;
+              code[U::NG * (cb & 7) + gb] = wb;
+            }
             if (tr == 0) {
               uint32_t* sc = reinterpret_cast<uint32_t*>(unit + (is_v ? U::OFF_VS : U::OFF_KS) + j * U::SCALE);
 #pragma unroll
@@ -265,22 +300,38 @@ __global__ void __launch_bounds__(kThreads) gather4_kernel(const GatherParams p)
     const page::Placed st = page::place_token(p.map, t, pos, pg, slot);
     if (st == page::kOutside) continue;
     if (st == page::kBad && lane == 0) page::flag_bad_page(p.status, page::kSiteGather);
-    for (int row = lane >> 3; row < rows; row += 4) {
-      const bool is_v = row >= p.Hkv;
-      const int h = is_v ? row - p.Hkv : row;
-      uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v : p.k) + ((long long)t * p.Hkv + h) * D) + i;
-      if (st != page::kFound) {
+    for (int row0 = lane >> 3; row0 < rows; row0 += 4 * kAhead) {
+      uint32_t w[kAhead][U::NG], sc[kAhead][U::NG];
+      uint4* dst[kAhead];
 #pragma unroll
-        for (int g = 0; g < U::NG; ++g) dst[8 * g] = make_uint4(0u, 0u, 0u, 0u);
-        continue;
+      for (int n = 0; n < kAhead; ++n) {
+        const int row = row0 + 4 * n;
+        if (row >= rows) break;
+        const bool is_v = row >= p.Hkv;
+        const int h = is_v ? row - p.Hkv : row;
+        dst[n] = reinterpret_cast<uint4*>((is_v ? p.v : p.k) + ((long long)t * p.Hkv + h) * D) + i;
+#pragma unroll
+        for (int g = 0; g < U::NG; ++g) w[n][g] = sc[n][g] = 0u;   // without a place: zeros
+        if (st != page::kFound) continue;
+        const uint8_t* unit =
+            p.pages + ((((long long)pg * p.Hkv + h) << (p.map.log_ps - 4)) + (slot >> 4)) * U::BYTES;
+        const int j = slot & 15;
+        const uint8_t* code = unit + (is_v ? U::OFF_VC : U::OFF_KC) + j * U::CODE + 4 * U::NG * i;
+        const uint8_t* scale = unit + (is_v ? U::OFF_VS : U::OFF_KS) + j * U::SCALE;
+        if constexpr (U::NG == 2) {
+          const uint2 a = __ldg(reinterpret_cast<const uint2*>(code)), b = __ldg(reinterpret_cast<const uint2*>(scale));
+          w[n][0] = a.x, w[n][1] = a.y, sc[n][0] = b.x, sc[n][1] = b.y;
+        } else {
+          w[n][0] = __ldg(reinterpret_cast<const uint32_t*>(code));
+          sc[n][0] = __ldg(reinterpret_cast<const uint32_t*>(scale));
+        }
       }
-      const uint8_t* unit =
-          p.pages + ((((long long)pg * p.Hkv + h) << (p.map.log_ps - 4)) + (slot >> 4)) * U::BYTES;
-      const int j = slot & 15;
-      const uint32_t* code = reinterpret_cast<const uint32_t*>(unit + (is_v ? U::OFF_VC : U::OFF_KC) + j * U::CODE);
-      const uint32_t* sc = reinterpret_cast<const uint32_t*>(unit + (is_v ? U::OFF_VS : U::OFF_KS) + j * U::SCALE);
 #pragma unroll
-      for (int g = 0; g < U::NG; ++g) dst[8 * g] = decode_word(code[U::NG * i + g], sc[g]);
+      for (int n = 0; n < kAhead; ++n) {
+        if (row0 + 4 * n >= rows) break;
+#pragma unroll
+        for (int g = 0; g < U::NG; ++g) dst[n][8 * g] = decode_word(w[n][g], sc[n][g]);
+      }
     }
   }
 }

@@ -26,10 +26,11 @@
 //
 // Work: the tiles (kTile tokens of one kv head) of all sequences form one line, cut into equal
 // parts, one per block, whatever the lengths.  A block's warps take its tiles in turn; each has
-// its own ring of bulk copies (a unit of 16 tokens is one run of bytes) and its own reference,
-// sum and output.  At the end of a (sequence, kv head) the block's warps join theirs through
-// shared memory; where the pair is shared with other blocks, each writes its part and the last
-// one to finish joins them (done flags with the call's tag, as attn_decode_kernel does).
+// its own ring of asynchronous copies, its own reference, sum and output, and waits for nobody.
+// (Copies are 16 bytes a lane: one bulk copy per unit, 2304 bytes, moved 4.3 TB/s at most.)
+// At the end of a (sequence, kv head) the block's warps join theirs through shared memory; where
+// the pair is shared with other blocks, each writes its part and the last one to finish joins
+// them (done flags with the call's tag, as attn_decode_kernel does).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -45,12 +46,10 @@ constexpr uint32_t kTopWeight = 0x7400u;         // 2^14 as fp16: a weight this 
 constexpr float kFirstWeight = 6.f;              // ... so that the largest becomes 2^6
 constexpr float kSmallStep = 9.313225746154785e-10f;  // 2^-30: smaller steps of V count as this in the reference
 
-enum : unsigned { kSiteFull = 0x520, kSiteDrain };
-
 // NT blocks of 8 heads per pass; a kv head with more than 8 query heads takes passes of 16.
 template <int D, int NT>
 struct Cfg {
-  static constexpr int W = 8;                 // warps
+  static constexpr int W = 8;  // warps
   static constexpr int NS = 2;                // ring stages of a warp
   static constexpr int THREADS = W * 32;
   static constexpr int HEADS = 8 * NT;
@@ -60,10 +59,9 @@ struct Cfg {
   static constexpr int OFF_L = OFF_O + W * HEADS * D * 4;        // [W][HEADS] fp32
   static constexpr int OFF_WT = OFF_L + W * HEADS * 4;           // [kMaxParts][HEADS] fp32
   static constexpr int kMaxParts = 160;                          // blocks that can share an item
-  static constexpr int OFF_BAR = OFF_WT + kMaxParts * HEADS * 4;
-  static constexpr int OFF_MISC = OFF_BAR + W * NS * 8;          // abort flag per warp, merge flag
-  static constexpr int SMEM_BYTES = OFF_MISC + W * 4 + 16;
-  static_assert(TILE_BYTES % 16 == 0 && OFF_BAR % 8 == 0 && SMEM_BYTES <= 227 * 1024, "shared memory");
+  static constexpr int OFF_MISC = OFF_WT + kMaxParts * HEADS * 4;  // merge flag
+  static constexpr int SMEM_BYTES = OFF_MISC + 16;
+  static_assert(TILE_BYTES % 16 == 0 && SMEM_BYTES <= 227 * 1024, "shared memory");
 };
 
 struct Params {
@@ -81,7 +79,6 @@ struct Params {
   float* lse;                 // [B][Hq]
   float scale_log2;
   unsigned* status;
-  unsigned long long timeout_ns;
 };
 
 // Token of a unit that row i (0..7) of the first product holds (row i + 8: 8 more).  The order
@@ -93,6 +90,10 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
+}
+// 16 bytes, global to shared, past L1.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
@@ -147,21 +148,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = lane >> 2, c = lane & 3;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * C::NS;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC) + warp;
-  volatile int* s_merge = reinterpret_cast<volatile int*>(smem + C::OFF_MISC) + W;
+  volatile int* s_merge = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
   float* s_o = reinterpret_cast<float*>(smem + C::OFF_O);
   float* s_l = reinterpret_cast<float*>(smem + C::OFF_L);
   float* s_wt = reinterpret_cast<float*>(smem + C::OFF_WT);
   const int nv = p.Hkv * p.RB;
-  const WaitCtl wc{p.status, abort_flag, p.timeout_ns};
-
-  if (lane == 0) {
-    *abort_flag = 0;
-    for (int i = 0; i < C::NS; ++i) mbar_init(&full[i], 1);
-    fence_mbar_init();
-  }
-  __syncwarp();
 
   // ---- this block's part [t0, t1) of the line, and where it starts (every warp by itself)
   int total = 0, longest = 0;
@@ -172,12 +163,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
   }
   total = __reduce_add_sync(0xffffffffu, total) * nv;
   longest = __reduce_max_sync(0xffffffffu, longest);
-  // Equal parts; while they are short, whole rounds of the warps, and no cut through sequences
-  // of at most two rounds: joining blocks costs more than a second round.
-  int chunk = (total + int(gridDim.x) - 1) / int(gridDim.x);
+  // Equal parts.  While they are short: whole rounds of the warps, and no cut through sequences
+  // of at most two rounds (joining blocks costs more than a second round).  With few sequences
+  // and heads, each begins at a block of its own: a block that ends one and begins the next
+  // would be last.
+  int chunk = max((total + int(gridDim.x) - 1) / int(gridDim.x), W);
   if (chunk < 4 * W) chunk = (chunk + W - 1) / W * W;
   if (longest <= 2 * W) chunk = max(chunk, longest);
-  const int t0 = min(total, int(blockIdx.x) * chunk), t1 = min(total, t0 + chunk);
+  const bool apart = p.B <= 32 && 4 * p.B * nv <= int(gridDim.x);
+  if (apart) {
+    const int n = lane < p.B ? tiles_of(length_of(p, lane)) : 0;
+    while (int(__reduce_add_sync(0xffffffffu, (n + chunk - 1) / chunk)) * nv > int(gridDim.x)) chunk += max(W, chunk / 16);
+    total = __reduce_add_sync(0xffffffffu, (n + chunk - 1) / chunk) * nv * chunk;
+  }
+  const int t0 = min(total, int(blockIdx.x) * chunk);
+  int t1 = min(total, t0 + chunk);
 
   // Sequences without tokens: o = 0, lse = -inf.
   for (int b = blockIdx.x; b < p.B; b += gridDim.x)
@@ -191,7 +191,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
   Cursor item;  // the (sequence, head block) the block is at; j counts from the item's own start
   for (int b0 = 0, before = 0;; b0 += 32) {
     const int L = b0 + lane < p.B ? length_of(p, b0 + lane) : 0;
-    const int n = tiles_of(L) * nv;
+    const int own = apart ? (tiles_of(L) + chunk - 1) / chunk * chunk : tiles_of(L);  // of the line, per head
+    const int n = own * nv;
     int incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -205,8 +206,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
       item.b = b0 + l;
       item.L = __shfl_sync(0xffffffffu, L, l);
       item.nt = tiles_of(item.L);
-      item.vh = off / item.nt;
-      item.j = off % item.nt;
+      const int each = __shfl_sync(0xffffffffu, own, l);
+      item.vh = off / each;
+      item.j = off % each;
+      if (apart) t1 = min(t1, t0 + item.nt - item.j);
       break;
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
@@ -214,50 +217,65 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
 
   // ---- this warp's copies: tiles t0 + warp, t0 + warp + W, ...
   uint8_t* ring = smem + C::OFF_RING + warp * C::NS * C::TILE_BYTES;
-  const int upp_log = p.log_ps - 4;                  // units of a page
-  const int step_log = min(upp_log, 31 - __clz(TU)); // units of one copy
+  const uint32_t ring_lane = smem_u32(ring) + lane * 16;
+  const int upp_log = p.log_ps - 4;                     // units of a page
   const long long page_bytes = ((long long)p.Hkv << upp_log) * U::BYTES;
   Cursor next = item;
   next.j += warp;
-  next.settle(p, nv);
-  int t_issue = t0 + warp;
-  int pg_next = 0;
-  const int lane_u = lane << step_log;               // first unit of this lane's copy
-  auto fetch_page = [&] {                            // page of this lane's copy of the next tile
-    const int u = next.j * TU + lane_u;
-    if (t_issue < t1 && lane_u < TU && u * page::kUnit < next.L)
-      pg_next = __ldg(p.table + (long long)next.b * p.width + (u >> upp_log));
+  int t_next = t0 + warp;
+  int pg[TU] = {};                                      // pages of the next tile's units
+  auto fetch_pages = [&] {
+    const int32_t* row = p.table + (long long)next.b * p.width;
+#pragma unroll
+    for (int i = 0; i < TU; ++i) {
+      const int u = next.j * TU + i;
+      if (u * page::kUnit < next.L) pg[i] = __ldg(row + (u >> upp_log));
+    }
   };
   auto issue = [&](int st) {
-    const int units = min(TU, ((next.L + page::kUnit - 1) >> 4) - next.j * TU);
-    if (lane == 0) mbar_arrive_expect_tx(&full[st], uint32_t(units) * U::BYTES);
-    __syncwarp();
-    if (lane_u < units) {
-      int pg = pg_next;
-      if (pg < 0 || pg >= p.num_pages) {
-        page::flag_bad_page(p.status, page::kSiteDecode4);
-        pg = 0;
-      }
+    if (t_next < t1) {
       const int g = p.RB == 1 ? next.vh : next.vh / p.RB;
-      const int u = (next.j * TU + lane_u) & ((1 << upp_log) - 1);
-      bulk_load(ring + st * C::TILE_BYTES + lane_u * U::BYTES,
-                p.pages + pg * page_bytes + ((g << upp_log) + u) * U::BYTES,
-                uint32_t(min(units - lane_u, 1 << step_log)) * U::BYTES, &full[st]);
+      const uint8_t* src[TU];
+#pragma unroll
+      for (int i = 0; i < TU; ++i) {
+        if (pg[i] < 0 || pg[i] >= p.num_pages) {
+          page::flag_bad_page(p.status, page::kSiteDecode4);
+          pg[i] = 0;
+        }
+        const int u = (next.j * TU + i) & ((1 << upp_log) - 1);
+        src[i] = p.pages + pg[i] * page_bytes + ((g << upp_log) + u) * U::BYTES;
+      }
+      const int units = min(TU, ((next.L + page::kUnit - 1) >> 4) - next.j * TU);
+      constexpr int CH = U::BYTES / 16;                 // 16-byte pieces of a unit
+      const uint32_t dst = ring_lane + st * C::TILE_BYTES;
+#pragma unroll
+      for (int k = 0; k < (TU * CH + 31) / 32; ++k) {
+        const int ch = k * 32 + lane;
+        const uint8_t* from = src[0] + ch * 16;
+#pragma unroll
+        for (int i = 1; i < TU; ++i)
+          if (ch >= i * CH) from = src[i] + (ch - i * CH) * 16;
+        if (ch < units * CH) copy16(dst + k * 512, from);
+      }
+      t_next += W;
+      next.j += W;
+      if (t_next < t1) {
+        next.settle(p, nv);
+        fetch_pages();
+      }
     }
-    t_issue += W;
-    next.j += W;
-    if (t_issue < t1) {
-      next.settle(p, nv);
-      fetch_page();
-    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  fetch_page();
-  for (int i = 0; i < C::NS && t_issue < t1; ++i) issue(i);
+  if (t_next < t1) {
+    next.settle(p, nv);
+    fetch_pages();
+  }
+#pragma unroll
+  for (int i = 0; i < C::NS; ++i) issue(i);
 
   // ---- tiles
-  int done = 0;             // tiles this warp has taken
+  int st = 0;                  // ring stage of this warp's next tile
   int t = t0, tw = t0 + warp;  // start of the item's part on the line; this warp's next tile
-  bool ok = true;
   const int key0 = token_of(r);
   while (t < t1) {
     const int e = min(t1, t + item.nt - item.j);         // end of the item's part
@@ -351,10 +369,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
       }
     }
 
-    for (bool first = true; tw < e; tw += W, ++done, first = false) {
-      const int st = done % C::NS;
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[st], (done / C::NS) & 1, wc, kSiteFull));
-      if (!ok) continue;
+    for (bool first = true; tw < e; tw += W, first = false, st = st + 1 == C::NS ? 0 : st + 1) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(C::NS - 1) : "memory");
+      __syncwarp();
       uint8_t* tile = ring + st * C::TILE_BYTES;
       const int left = L - (item.j + (tw - t)) * kTile;   // tokens from the tile's first on
       if (left < kTile) {
@@ -552,7 +569,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
         }
       }
       __syncwarp();  // every lane has read the stage
-      if (t_issue < t1) issue(st);
+      issue(st);
     }
 
     // ---- join the warps' parts of this item: normalised outputs, log2 sums
@@ -590,13 +607,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
     const long long row0 = (long long)item.b * p.Hq + h0;
     const int nw = min(W, e - t);                               // warps that had a tile
     const int w0 = (t - t0) % W;                                // the first of them
-    for (int i = tid; i < nh * (D / 4); i += C::THREADS) {
+    for (int i = tid; i < nh * (D / 4); i += W * 32) {
       const int h = i / (D / 4), d4 = i % (D / 4);
       float M = -INFINITY;
+#pragma unroll 4
       for (int k = 0; k < nw; ++k) M = fmaxf(M, s_l[((w0 + k) % W) * C::HEADS + h]);
       const float Mz = M == -INFINITY ? 0.f : M;
       float l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
       for (int k = 0; k < nw; ++k) {
         const int w = (w0 + k) % W;
         const float y = ex2_approx(s_l[w * C::HEADS + h] - Mz);
@@ -638,37 +657,60 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
         __threadfence();
         const int parts = c1 - c0 + 1;
         for (int h = warp; h < nh; h += W) {   // the parts' weights, a warp per head
-          float M = -INFINITY, l = 0.f;
-          for (int k = lane; k < parts; k += 32) M = fmaxf(M, __ldcg(p.l_part + (long long)slot_of(c0 + k) * C::HEADS + h));
+          constexpr int K = C::kMaxParts / 32;
+          float y[K], M = -INFINITY, l = 0.f;
+#pragma unroll
+          for (int i = 0; i < K; ++i) {
+            const int k = lane + 32 * i;
+            y[i] = k < parts ? __ldcg(p.l_part + (long long)slot_of(c0 + k) * C::HEADS + h) : -INFINITY;
+            M = fmaxf(M, y[i]);
+          }
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
           const float Mz = M == -INFINITY ? 0.f : M;
-          for (int k = lane; k < parts; k += 32) {
-            const float y = ex2_approx(__ldcg(p.l_part + (long long)slot_of(c0 + k) * C::HEADS + h) - Mz);
-            s_wt[k * C::HEADS + h] = y;
-            l += y;
+#pragma unroll
+          for (int i = 0; i < K; ++i) {
+            y[i] = ex2_approx(y[i] - Mz);
+            l += y[i];
           }
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-          if (lane == 0) {
-            s_l[h] = l == 0.f ? 0.f : 1.f / l;
-            p.lse[row0 + h] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994530942f;
-          }
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+          for (int i = 0; i < K; ++i)
+            if (lane + 32 * i < parts) s_wt[(lane + 32 * i) * C::HEADS + h] = y[i] * inv;
+          if (lane == 0) p.lse[row0 + h] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994530942f;
         }
         __syncthreads();
-        for (int i = tid; i < nh * (D / 4); i += C::THREADS) {
+        // Columns of four elements; the threads left over share a column's parts.
+        const int cols = nh * (D / 4);
+        const int share = W * 32 / cols > 1 ? min(W * 32 / cols, 4) : 1;
+        for (int i0 = 0; i0 < cols; i0 += W * 32) {
+          const int sub = share > 1 ? tid / cols : 0;
+          const int i = share > 1 ? tid % cols : i0 + tid;
           const int h = i / (D / 4), d4 = i % (D / 4);
           float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (sub < share && i < cols) {
+            const float4* src = reinterpret_cast<const float4*>(p.o_part) + (long long)h * (D / 4) + d4;
 #pragma unroll 8
-          for (int k = 0; k < parts; ++k) {
-            const float y = s_wt[k * C::HEADS + h];
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.o_part) +
-                                    ((long long)slot_of(c0 + k) * C::HEADS + h) * (D / 4) + d4);
-            o.x = fmaf(y, v.x, o.x), o.y = fmaf(y, v.y, o.y), o.z = fmaf(y, v.z, o.z), o.w = fmaf(y, v.w, o.w);
+            for (int k = sub; k < parts; k += share) {
+              const float y = s_wt[k * C::HEADS + h];
+              const float4 v = __ldcg(src + (long long)slot_of(c0 + k) * (C::HEADS * (D / 4)));
+              o.x = fmaf(y, v.x, o.x), o.y = fmaf(y, v.y, o.y), o.z = fmaf(y, v.z, o.z), o.w = fmaf(y, v.w, o.w);
+            }
           }
-          const float inv = s_l[h];
-          reinterpret_cast<uint2*>(p.o)[(row0 + h) * (D / 4) + d4] =
-              make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+          if (share > 1) {
+            if (sub > 0 && sub < share) reinterpret_cast<float4*>(s_o)[(sub - 1) * cols + i] = o;
+            __syncthreads();
+            if (sub == 0)
+              for (int k = 0; k < share - 1; ++k) {
+                const float4 v = reinterpret_cast<const float4*>(s_o)[k * cols + i];
+                o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+              }
+          }
+          if (sub == 0 && i < cols)
+            reinterpret_cast<uint2*>(p.o)[(row0 + h) * (D / 4) + d4] =
+                make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
         }
       }
     }
@@ -677,13 +719,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
     item.j += e - t;
     t = e;
     if (t < t1) item.settle(p, nv);
-  }
-
-  // Copies still in flight (only when a wait gave up) land before shared memory is released.
-  if (!ok && lane == 0) {
-    const int n = (t_issue - t0 - warp) / W;   // tiles issued
-    for (int k = max(0, n - C::NS); k < n; ++k)
-      mbar_drain_checked(&full[k % C::NS], (k / C::NS) & 1, wc, kSiteDrain);
   }
 }
 

@@ -478,6 +478,18 @@ attn_status append_params(append::Params* p, const void* q, const void* k, const
 
 unsigned grid_of(long long need, unsigned most) { return unsigned(need < most ? need : most); }
 
+// A warp per token; where that leaves the SMs' 32 warps idle, up to 8 share a token's rows.
+unsigned append_grid(append::Params* p, int D, unsigned sms) {
+  const int per_pass = 32 / (D / 16), rows = p->nq + 2 * p->Hkv;
+  const long long wave = (long long)sms * 32;
+  p->share_log = 0;
+  while (p->share_log < 3 && ((long long)p->map.T << (p->share_log + 1)) <= wave && (per_pass << p->share_log) < rows)
+    ++p->share_log;
+  const long long warps = (long long)p->map.T << p->share_log;
+  const int per_block = append::kThreads / 32;
+  return grid_of((warps + per_block - 1) / per_block, sms * 8);
+}
+
 // Plan of the 4-bit decode: one block per SM, fewer where the longest possible batch has no
 // tile for every warp.  Up to 8 query heads of a kv head take one pass of 8, more take passes
 // of 16.  The workspace holds two shared parts per block.
@@ -492,8 +504,7 @@ Decode4Ws decode4_ws(int B, int Hq, int Hkv, int D, int Lmax) {
   const int G = Hq / Hkv;
   w.nt = G <= 8 ? 1 : 2;
   const int heads = 8 * w.nt;
-  constexpr int warps = decode4::Cfg<128, 1>::W;
-  static_assert(warps == decode4::Cfg<128, 2>::W, "one plan for both");
+  const int warps = w.nt == 1 ? decode4::Cfg<128, 1>::W : decode4::Cfg<128, 2>::W;
   static_assert(kPlanSMs <= decode4::Cfg<128, 1>::kMaxParts, "blocks that can share an item");
   w.passes = (G + heads - 1) / heads;
   w.tiles = (long long)((Lmax + decode4::kTile - 1) / decode4::kTile) * B * Hkv * w.passes;
@@ -886,7 +897,6 @@ attn_status attn_decode_kv4(const void* q, const void* pages, const int32_t* blo
   p.lse = lse;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.status = dev->status;
-  p.timeout_ns = g_timeout_ns.load();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto launch = [&](auto kernel, auto cfg) {
     kernel<<<w.grid, cfg.THREADS, cfg.SMEM_BYTES, s>>>(p);
@@ -919,7 +929,7 @@ attn_status attn_append_kv(const void* q, const void* k, const void* v, long lon
   p.k_pages = static_cast<__nv_bfloat16*>(k_pages);
   p.v_pages = static_cast<__nv_bfloat16*>(v_pages);
   p.status = dev->status;
-  const unsigned grid = grid_of(T, dev->sms * 8);
+  const unsigned grid = append_grid(&p, D, dev->sms);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (D == 64) append::append_kernel<64, false><<<grid, append::kThreads, 0, s>>>(p);
   else append::append_kernel<128, false><<<grid, append::kThreads, 0, s>>>(p);
@@ -946,7 +956,7 @@ attn_status attn_append_kv4(const void* q, const void* k, const void* v, long lo
   if ((st = device_setup(&dev, k)) != ATTN_OK) return st;
   p.pages = static_cast<uint8_t*>(pages);
   p.status = dev->status;
-  const unsigned grid = grid_of(T, dev->sms * 8);
+  const unsigned grid = append_grid(&p, D, dev->sms);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (D == 64) append::append_kernel<64, true><<<grid, append::kThreads, 0, s>>>(p);
   else append::append_kernel<128, true><<<grid, append::kThreads, 0, s>>>(p);

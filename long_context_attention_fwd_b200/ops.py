@@ -33,7 +33,8 @@ MERGE_MAX_PARTS = 16  # ATTN_MERGE_MAX_PARTS of the C ABI
 
 
 def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    # the raw handle, without building a Stream object (3 us a call)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _dims(q: torch.Tensor, k: torch.Tensor, cu_seqlens: Optional[torch.Tensor],
@@ -306,90 +307,97 @@ def _check_kv4(pages: torch.Tensor):
     """(num_pages, Hkv, page_size, D) of a pool of 4-bit pages."""
     if not pages.is_cuda:
         raise ValueError("libattn needs CUDA tensors (there is no CPU path)")
-    if pages.dim() != 4 or pages.dtype != torch.uint8 or pages.shape[3] not in (18 * 64, 18 * 128) \
+    shape = pages.shape
+    if len(shape) != 4 or pages.dtype != torch.uint8 or shape[3] not in (18 * 64, 18 * 128) \
             or not pages.is_contiguous():
         raise ValueError("pages must be contiguous uint8 [num_pages, Hkv, page_size / 16, 18 D]")
-    P, Hkv, units, row = pages.shape
-    return P, Hkv, units * KV4_UNIT, row // 18
+    return shape[0], shape[1], shape[2] * KV4_UNIT, shape[3] // 18
 
 
 def _check_paged(k_pages: torch.Tensor, v_pages: torch.Tensor):
     """(num_pages, Hkv, page_size, D) of a pool of bf16 pages."""
     _check_inputs(k_pages, v_pages)
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
-        raise ValueError("k_pages and v_pages must be [num_pages, page_size, Hkv, D]")
-    P, ps, Hkv, D = k_pages.shape
-    return P, Hkv, ps, D
+    shape = k_pages.shape
+    if len(shape) != 4 or v_pages.shape != shape or v_pages.device != k_pages.device:
+        raise ValueError("k_pages and v_pages must be [num_pages, page_size, Hkv, D] on one device")
+    return shape[0], shape[2], shape[1], shape[3]
 
 
-def _check_int32(t: torch.Tensor, name: str, dim: int) -> None:
-    if t.dtype != torch.int32 or not t.is_cuda or t.dim() != dim or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dim}-D int32 CUDA tensor")
+def _check_int32(t: torch.Tensor, name: str, dim: int, device) -> None:
+    if t.dtype != torch.int32 or t.device != device or t.dim() != dim or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dim}-D int32 tensor on {device}")
 
 
-def _check_map(block_table, cache_len, cu_seqlens, device) -> int:
-    """Checks the arrays that place tokens; returns the number of sequences."""
-    _check_int32(block_table, "block_table", 2)
-    _check_int32(cache_len, "cache_len", 1)
-    B = cache_len.shape[0]
-    if block_table.shape[0] != B:
+def _check_map(block_table, cache_len, cu_seqlens, device):
+    """Checks the arrays that place tokens; returns (sequences, pages of a table row)."""
+    _check_int32(block_table, "block_table", 2, device)
+    _check_int32(cache_len, "cache_len", 1, device)
+    B, width = block_table.shape
+    if cache_len.shape[0] != B:
         raise ValueError("block_table needs a row for each entry of cache_len")
     if cu_seqlens is not None:
-        _check_int32(cu_seqlens, "cu_seqlens", 1)
+        _check_int32(cu_seqlens, "cu_seqlens", 1, device)
         if cu_seqlens.shape[0] != B + 1:
             raise ValueError("cu_seqlens needs one entry more than cache_len")
-    _same_device(device, block_table, cache_len, cu_seqlens)
-    return B
+    return B, width
 
 
-def _check_rows(t: torch.Tensor, name: str, T: int, H: int, D: int, device) -> None:
-    """A [T, H, D] bf16 tensor whose tokens may lie any multiple of 8 elements apart (a
-    slice of a projection that holds q, k and v side by side)."""
+def _check_rows(t: torch.Tensor, name: str, shape, device) -> int:
+    """Checks a [T, H, D] bf16 tensor whose tokens may lie any multiple of 8 elements apart (a
+    slice of a projection that holds q, k and v side by side); returns that distance."""
     if t.dtype != torch.bfloat16:
         raise ValueError("tensors must be bfloat16")
-    if tuple(t.shape) != (T, H, D) or t.device != device:
-        raise ValueError(f"{name} must be {(T, H, D)} on {device}")
-    if T and (t.stride(2) != 1 or (H > 1 and t.stride(1) != D) or (T > 1 and t.stride(0) % 8)):
+    if t.shape != shape or t.device != device:
+        raise ValueError(f"{name} must be {tuple(shape)} on {device}")
+    T, H, D = shape
+    apart, head, one = t.stride()
+    if T and (one != 1 or (H > 1 and head != D) or (T > 1 and apart % 8)):
         raise ValueError(f"{name}: heads must be contiguous and tokens a multiple of 8 elements apart")
+    return apart if T > 1 else H * D
 
 
-def _append_args(k, v, block_table, cache_len, q, rope, cu_seqlens, q_out, Hkv, D, device):
-    """Checks shared by the two appends; returns (arguments up to q_out, B, T, Hq, q_out)."""
+def _append_args(k, v, block_table, cache_len, q, rope, interleaved, cu_seqlens, q_out, Hkv, D, device):
+    """Checks shared by the two appends; returns (the arguments before the pages, those after
+    them up to D, the table's width, q_out)."""
     if k.dim() != 3:
         raise ValueError("k must be [T, Hkv, D]")
     T = k.shape[0]
-    B = _check_map(block_table, cache_len, cu_seqlens, device)
+    B, width = _check_map(block_table, cache_len, cu_seqlens, device)
     if cu_seqlens is None and T != B:
         raise ValueError("without cu_seqlens there is one token per sequence")
-    _check_rows(k, "k", T, Hkv, D, device)
-    _check_rows(v, "v", T, Hkv, D, device)
-    Hq, cos, sin, rope_len, rope_dim = 0, None, None, 0, 0
+    shape = torch.Size((T, Hkv, D))
+    k_stride, v_stride = _check_rows(k, "k", shape, device), _check_rows(v, "v", shape, device)
+    Hq = q_stride = rope_len = rope_dim = 0
+    cos = sin = q_ptr = q_out_ptr = None
     if rope is not None:
-        cos, sin = rope
-        if cos.dim() != 2 or 2 * cos.shape[1] > D:
+        rc, rs = rope
+        if rc.dim() != 2:
             raise ValueError("rope must be (cos, sin), each [positions, rotated elements / 2]")
-        _check_tensor(cos, "rope[0]", cos.shape, torch.float32, device)
-        _check_tensor(sin, "rope[1]", cos.shape, torch.float32, device)
-        rope_len, rope_dim = cos.shape[0], 2 * cos.shape[1]
-        if rope_dim < 16 or rope_dim % 16:
-            raise ValueError("the number of rotated elements must be a multiple of 16")
+        _check_tensor(rc, "rope[0]", rc.shape, torch.float32, device)
+        _check_tensor(rs, "rope[1]", rc.shape, torch.float32, device)
+        rope_len, rope_dim = rc.shape[0], 2 * rc.shape[1]
+        if rope_dim > D or rope_dim < 16 or rope_dim % 16:
+            raise ValueError("the number of rotated elements must be a multiple of 16 up to D")
+        cos, sin = rc.data_ptr(), rs.data_ptr()
     if q is not None:
         if rope is None:
             raise ValueError("q is only rotated: it needs rope")
         if q.dim() != 3:
             raise ValueError("q must be [T, Hq, D]")
         Hq = q.shape[1]
-        _check_rows(q, "q", T, Hq, D, device)
-        _check_tensor(q_out, "q_out", (T, Hq, D), torch.bfloat16, device)
+        shape = torch.Size((T, Hq, D))
+        q_stride = _check_rows(q, "q", shape, device)
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=device)
+            q_out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        else:
+            _check_tensor(q_out, "q_out", shape, torch.bfloat16, device)
+        q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    stride = lambda t: t.stride(0) if T > 1 else t.shape[1] * D  # noqa: E731
-    ptr = lambda t: None if t is None else t.data_ptr()          # noqa: E731
-    args = (ptr(q), k.data_ptr(), v.data_ptr(), 0 if q is None else stride(q), stride(k), stride(v),
-            ptr(cos), ptr(sin), rope_len, rope_dim)
-    return args, B, T, Hq, q_out
+    before = (q_ptr, k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride, cos, sin, rope_len,
+              rope_dim, interleaved, None if cu_seqlens is None else cu_seqlens.data_ptr(),
+              cache_len.data_ptr(), block_table.data_ptr(), q_out_ptr)
+    return before, (B, T, Hq, Hkv, D), width, q_out
 
 
 def attn_append_kv(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -415,15 +423,11 @@ def attn_append_kv(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pa
     then reports an invalid argument.  Two tokens that share a place leave either's value."""
     P, Hkv, ps, D = _check_paged(k_pages, v_pages)
     dev = k_pages.device
-    args, B, T, Hq, q_out = _append_args(k, v, block_table, cache_len, q, rope, cu_seqlens, q_out,
-                                         Hkv, D, dev)
-    _same_device(dev, v_pages)
-    if T:
-        capi.check(capi.attn_append_kv(
-            *args, interleaved, None if cu_seqlens is None else cu_seqlens.data_ptr(),
-            cache_len.data_ptr(), block_table.data_ptr(), None if q is None else q_out.data_ptr(),
-            k_pages.data_ptr(), v_pages.data_ptr(), B, T, Hq, Hkv, D, block_table.shape[1], P, ps,
-            _stream(dev)), "attn_append_kv")
+    before, sizes, width, q_out = _append_args(k, v, block_table, cache_len, q, rope, interleaved,
+                                               cu_seqlens, q_out, Hkv, D, dev)
+    if sizes[1]:
+        capi.check(capi.attn_append_kv(*before, k_pages.data_ptr(), v_pages.data_ptr(), *sizes,
+                                       width, P, ps, _stream(dev)), "attn_append_kv")
     return q_out
 
 
@@ -438,14 +442,11 @@ def attn_append_kv4(k: torch.Tensor, v: torch.Tensor, pages: torch.Tensor,
     clamp(round((x - m) / s), 0, 15); a group with a NaN or an infinity reads back as NaN."""
     P, Hkv, ps, D = _check_kv4(pages)
     dev = pages.device
-    args, B, T, Hq, q_out = _append_args(k, v, block_table, cache_len, q, rope, cu_seqlens, q_out,
-                                         Hkv, D, dev)
-    if T:
-        capi.check(capi.attn_append_kv4(
-            *args, interleaved, None if cu_seqlens is None else cu_seqlens.data_ptr(),
-            cache_len.data_ptr(), block_table.data_ptr(), None if q is None else q_out.data_ptr(),
-            pages.data_ptr(), B, T, Hq, Hkv, D, block_table.shape[1], P, ps, _stream(dev)),
-            "attn_append_kv4")
+    before, sizes, width, q_out = _append_args(k, v, block_table, cache_len, q, rope, interleaved,
+                                               cu_seqlens, q_out, Hkv, D, dev)
+    if sizes[1]:
+        capi.check(capi.attn_append_kv4(*before, pages.data_ptr(), *sizes, width, P, ps, _stream(dev)),
+                   "attn_append_kv4")
     return q_out
 
 
@@ -461,16 +462,16 @@ def attn_gather_kv4(pages: torch.Tensor, block_table: torch.Tensor, cache_len: t
     dev = pages.device
     if cu_seqlens is None or T < 0:
         raise ValueError("attn_gather_kv4 needs cu_seqlens and T >= 0")
-    B = _check_map(block_table, cache_len, cu_seqlens, dev)
-    _check_tensor(k, "k", (T, Hkv, D), torch.bfloat16, dev)
-    _check_tensor(v, "v", (T, Hkv, D), torch.bfloat16, dev)
-    k = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=dev) if k is None else k
-    v = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=dev) if v is None else v
+    B, width = _check_map(block_table, cache_len, cu_seqlens, dev)
+    shape = (T, Hkv, D)
+    _check_tensor(k, "k", shape, torch.bfloat16, dev)
+    _check_tensor(v, "v", shape, torch.bfloat16, dev)
+    k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
+    v = torch.empty_like(k) if v is None else v
     if T:
         capi.check(capi.attn_gather_kv4(
             pages.data_ptr(), block_table.data_ptr(), cache_len.data_ptr(), cu_seqlens.data_ptr(),
-            k.data_ptr(), v.data_ptr(), B, T, Hkv, D, block_table.shape[1], P, ps, _stream(dev)),
-            "attn_gather_kv4")
+            k.data_ptr(), v.data_ptr(), B, T, Hkv, D, width, P, ps, _stream(dev)), "attn_gather_kv4")
     return k, v
 
 
@@ -488,24 +489,31 @@ def attn_decode_kv4_workspace_size(q: torch.Tensor, pages: torch.Tensor,
                                                pages.shape[2] * KV4_UNIT)
 
 
-def _decode_args(q, D, block_table, cache_len, scale, out, lse, workspace, need, device):
+def _decode_args(q, Hkv, ps, D, block_table, cache_len, scale, out, lse, workspace, size, device):
     """Checks and outputs shared by the two paged decodes."""
     _check_inputs(q)
     if q.dim() != 3 or q.shape[2] != D:
         raise ValueError("q must be [B, Hq, D] with the cache's D")
-    B = _check_map(block_table, cache_len, None, device)
-    if q.shape[0] != B:
-        raise ValueError("q needs a row for each entry of cache_len")
-    _same_device(device, q)
+    B, width = _check_map(block_table, cache_len, None, device)
+    Bq, Hq, _ = q.shape
+    if Bq != B or q.device != device:
+        raise ValueError(f"q needs a row for each entry of cache_len, on {device}")
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    _check_tensor(out, "out", q.shape, torch.bfloat16, device)
-    _check_tensor(lse, "lse", q.shape[:2], torch.float32, device)
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=device) if lse is None else lse
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_tensor(out, "out", q.shape, torch.bfloat16, device)
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=device)
+    else:
+        _check_tensor(lse, "lse", (B, Hq), torch.float32, device)
     if workspace is None:
-        workspace = torch.empty(max(need(), 1), dtype=torch.uint8, device=device)
-    return scale, out, lse, workspace, _workspace_bytes(workspace, device)
+        nbytes = size(B, Hq, Hkv, D, width, ps)
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    else:
+        nbytes = _workspace_bytes(workspace, device)
+    return scale, out, lse, workspace, nbytes, B, Hq, width
 
 
 def attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -520,15 +528,13 @@ def attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Ten
     attn_device_status and leaves that sequence's result unspecified."""
     P, Hkv, ps, D = _check_paged(k_pages, v_pages)
     dev = k_pages.device
-    _same_device(dev, v_pages)
-    scale, out, lse, workspace, nbytes = _decode_args(
-        q, D, block_table, cache_len, scale, out, lse, workspace,
-        lambda: attn_decode_paged_workspace_size(q, k_pages, block_table), dev)
-    B, Hq, _ = q.shape
+    scale, out, lse, workspace, nbytes, B, Hq, width = _decode_args(
+        q, Hkv, ps, D, block_table, cache_len, scale, out, lse, workspace,
+        capi.attn_decode_paged_workspace_size, dev)
     capi.check(capi.attn_decode_paged(
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
-        cache_len.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, D, block_table.shape[1],
-        P, ps, scale, workspace.data_ptr(), nbytes, _stream(dev)), "attn_decode_paged")
+        cache_len.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, D, width, P, ps, scale,
+        workspace.data_ptr(), nbytes, _stream(dev)), "attn_decode_paged")
     return out, lse
 
 
@@ -540,14 +546,13 @@ def attn_decode_kv4(q: torch.Tensor, pages: torch.Tensor, block_table: torch.Ten
     of q over the values s * code + m that the pages stand for."""
     P, Hkv, ps, D = _check_kv4(pages)
     dev = pages.device
-    scale, out, lse, workspace, nbytes = _decode_args(
-        q, D, block_table, cache_len, scale, out, lse, workspace,
-        lambda: attn_decode_kv4_workspace_size(q, pages, block_table), dev)
-    B, Hq, _ = q.shape
+    scale, out, lse, workspace, nbytes, B, Hq, width = _decode_args(
+        q, Hkv, ps, D, block_table, cache_len, scale, out, lse, workspace,
+        capi.attn_decode_kv4_workspace_size, dev)
     capi.check(capi.attn_decode_kv4(
         q.data_ptr(), pages.data_ptr(), block_table.data_ptr(), cache_len.data_ptr(),
-        out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, D, block_table.shape[1], P, ps, scale,
-        workspace.data_ptr(), nbytes, _stream(dev)), "attn_decode_kv4")
+        out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, D, width, P, ps, scale, workspace.data_ptr(),
+        nbytes, _stream(dev)), "attn_decode_kv4")
     return out, lse
 
 
