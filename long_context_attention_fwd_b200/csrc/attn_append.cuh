@@ -27,7 +27,7 @@ namespace attn_sm100 {
 namespace append {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 3;  // rows a thread has in flight
+constexpr int kAhead = 2;  // rows a thread has in flight
 
 struct Params {
   page::PageMap map;
@@ -97,23 +97,27 @@ __device__ __forceinline__ uint32_t encode(const Chunk& c, float m, float s) {
     }
     return w;
   }
+  // The fma rounds a / s to a whole number in the low bits of its result.  1 / s is off by 2^-24,
+  // so it errs only where a / s is within 2^-20 of a half; there the remainder decides.  No
+  // clamp: a <= 15 s (1 + 2^-8).
   const float inv = __frcp_rn(s), half = 0.5f * s;
+  constexpr float kWhole = 8388608.f;  // 2^23
+  float t[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float a = __fsub_rn(c.x[j], m);        // >= 0: m is the group's minimum
-    const float t = fminf(rintf(a * inv), 15.f);
-    const float rem = fmaf(-t, s, a);            // exact: t s has 12 bits, and a is near it
-    int q = int(t);
-    const bool odd = q & 1;
-    if (rem > half || (rem == half && odd)) ++q;
-    if (rem < -half || (rem == -half && odd)) --q;
-    w |= uint32_t(min(q, 15)) << (4 * j);
+    const float z = fmaf(a, inv, kWhole);
+    t[j] = z - kWhole;
+    const float rem = fmaf(-t[j], s, a);         // exact: t s has 12 bits, and a is near it
+    if (fabsf(rem) >= half && (fabsf(rem) > half || (__float_as_uint(z) & 1u))) t[j] += rem > 0.f ? 1.f : -1.f;
   }
-  return w;
+  const float lo = fmaf(4096.f, t[3], fmaf(256.f, t[2], fmaf(16.f, t[1], t[0]))) + kWhole;
+  const float hi = fmaf(4096.f, t[7], fmaf(256.f, t[6], fmaf(16.f, t[5], t[4]))) + kWhole;
+  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410);
 }
 
 template <int D, bool KV4>
-__global__ void __launch_bounds__(kThreads) append_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(const Params p) {
   constexpr int TPR = D / 16;            // threads of a row
   constexpr int RPP = 32 / TPR;          // rows of a warp's pass
   const int lane = threadIdx.x & 31;
@@ -210,21 +214,27 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Params p) {
           const Chunk a = unpack(u[i][0]), b = unpack(u[i][1]);
           const int ga = ca / 8, gb = cb / 8;
           float lo[U::NG], hi[U::NG];
+          float la = a.x[0], ha = a.x[0], lb = b.x[0], hb = b.x[0];
 #pragma unroll
-          for (int g = 0; g < U::NG; ++g) {
-            lo[g] = INFINITY;
-            hi[g] = -INFINITY;
+          for (int j = 1; j < 8; ++j) {
+            la = min_nan(la, a.x[j]), ha = max_nan(ha, a.x[j]);
+            lb = min_nan(lb, b.x[j]), hb = max_nan(hb, b.x[j]);
+          }
+          if constexpr (U::NG == 1) {
+            lo[0] = min_nan(la, lb), hi[0] = max_nan(ha, hb);
+          } else {
+            const bool one = ga == gb;               // both chunks in one group
+            const float l = one ? min_nan(la, lb) : la, h2 = one ? max_nan(ha, hb) : ha;
+            lo[0] = ga == 0 ? l : INFINITY, hi[0] = ga == 0 ? h2 : -INFINITY;
+            lo[1] = ga == 1 ? l : one ? INFINITY : lb, hi[1] = ga == 1 ? h2 : one ? -INFINITY : hb;
+          }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              if (ga == g) lo[g] = min_nan(lo[g], a.x[j]), hi[g] = max_nan(hi[g], a.x[j]);
-              if (gb == g) lo[g] = min_nan(lo[g], b.x[j]), hi[g] = max_nan(hi[g], b.x[j]);
-            }
+          for (int g = 0; g < U::NG; ++g)
 #pragma unroll
             for (int o = 1; o < TPR; o <<= 1) {
               lo[g] = min_nan(lo[g], __shfl_xor_sync(0xffffffffu, lo[g], o));
               hi[g] = max_nan(hi[g], __shfl_xor_sync(0xffffffffu, hi[g], o));
             }
-          }
           uint32_t sm[U::NG];
           float step[U::NG];
 #pragma unroll
@@ -239,15 +249,15 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Params p) {
             }
           }
           if (live && hv >= 0) {
-            const float la = (U::NG == 2 && ga) ? lo[U::NG - 1] : lo[0];
-            const float lb = (U::NG == 2 && gb) ? lo[U::NG - 1] : lo[0];
+            const float ma = (U::NG == 2 && ga) ? lo[U::NG - 1] : lo[0];
+            const float mb = (U::NG == 2 && gb) ? lo[U::NG - 1] : lo[0];
             const float sa = (U::NG == 2 && ga) ? step[U::NG - 1] : step[0];
             const float sb = (U::NG == 2 && gb) ? step[U::NG - 1] : step[0];
             const int upp_log = p.map.log_ps - 4;
             uint8_t* unit = p.pages + ((((long long)pg * p.Hkv + h) << upp_log) + (slot >> 4)) * U::BYTES;
             const int j = slot & 15;
             uint32_t* code = reinterpret_cast<uint32_t*>(unit + (is_v ? U::OFF_VC : U::OFF_KC) + j * U::CODE);
-            const uint32_t wa = encode(a, la, sa), wb = encode(b, lb, sb);
+            const uint32_t wa = encode(a, ma, sa), wb = encode(b, mb, sb);
             if (U::NG == 2 && cb == ca + 8) {   // the same word of both groups: neighbours
               *reinterpret_cast<uint2*>(code + 2 * ca) = make_uint2(wa, wb);
             } else {
@@ -269,7 +279,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Params p) {
 // gather4_kernel: packed token t's K and V out of 4-bit pages, x = s * code + m in fp32 (the
 // product is exact: 8 bits by 4), rounded once to bf16.  One warp takes a token; eight threads
 // hold a row, each the word (or the two words of both groups) of eight elements, so that reads
-// and writes are whole sectors.  Bound by HBM, by the bf16 rows it writes.
+// and writes are whole sectors.  Bound by HBM, by the bf16 rows it writes; with one row a lane in
+// flight 32 registers let all 64 warps of an SM in, which measured faster than three rows and 40.
 struct GatherParams {
   page::PageMap map;
   const uint8_t* pages;
@@ -288,7 +299,7 @@ __device__ __forceinline__ uint4 decode_word(uint32_t w, uint32_t sm) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) gather4_kernel(const GatherParams p) {
+__global__ void __launch_bounds__(kThreads, 8) gather4_kernel(const GatherParams p) {
   using U = page::Unit<D>;
   const int warp = (blockIdx.x * kThreads + threadIdx.x) >> 5;
   const int nwarp = gridDim.x * (kThreads / 32);
@@ -300,38 +311,27 @@ __global__ void __launch_bounds__(kThreads) gather4_kernel(const GatherParams p)
     const page::Placed st = page::place_token(p.map, t, pos, pg, slot);
     if (st == page::kOutside) continue;
     if (st == page::kBad && lane == 0) page::flag_bad_page(p.status, page::kSiteGather);
-    for (int row0 = lane >> 3; row0 < rows; row0 += 4 * kAhead) {
-      uint32_t w[kAhead][U::NG], sc[kAhead][U::NG];
-      uint4* dst[kAhead];
-#pragma unroll
-      for (int n = 0; n < kAhead; ++n) {
-        const int row = row0 + 4 * n;
-        if (row >= rows) break;
-        const bool is_v = row >= p.Hkv;
-        const int h = is_v ? row - p.Hkv : row;
-        dst[n] = reinterpret_cast<uint4*>((is_v ? p.v : p.k) + ((long long)t * p.Hkv + h) * D) + i;
-#pragma unroll
-        for (int g = 0; g < U::NG; ++g) w[n][g] = sc[n][g] = 0u;   // without a place: zeros
-        if (st != page::kFound) continue;
+    for (int row = lane >> 3; row < rows; row += 4) {
+      const bool is_v = row >= p.Hkv;
+      const int h = is_v ? row - p.Hkv : row;
+      uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v : p.k) + ((long long)t * p.Hkv + h) * D) + i;
+      uint2 w = make_uint2(0u, 0u), sc = make_uint2(0u, 0u);   // without a place: zeros
+      if (st == page::kFound) {
         const uint8_t* unit =
             p.pages + ((((long long)pg * p.Hkv + h) << (p.map.log_ps - 4)) + (slot >> 4)) * U::BYTES;
         const int j = slot & 15;
         const uint8_t* code = unit + (is_v ? U::OFF_VC : U::OFF_KC) + j * U::CODE + 4 * U::NG * i;
         const uint8_t* scale = unit + (is_v ? U::OFF_VS : U::OFF_KS) + j * U::SCALE;
         if constexpr (U::NG == 2) {
-          const uint2 a = __ldg(reinterpret_cast<const uint2*>(code)), b = __ldg(reinterpret_cast<const uint2*>(scale));
-          w[n][0] = a.x, w[n][1] = a.y, sc[n][0] = b.x, sc[n][1] = b.y;
+          w = *reinterpret_cast<const uint2*>(code);
+          sc = *reinterpret_cast<const uint2*>(scale);
         } else {
-          w[n][0] = __ldg(reinterpret_cast<const uint32_t*>(code));
-          sc[n][0] = __ldg(reinterpret_cast<const uint32_t*>(scale));
+          w.x = *reinterpret_cast<const uint32_t*>(code);
+          sc.x = *reinterpret_cast<const uint32_t*>(scale);
         }
       }
-#pragma unroll
-      for (int n = 0; n < kAhead; ++n) {
-        if (row0 + 4 * n >= rows) break;
-#pragma unroll
-        for (int g = 0; g < U::NG; ++g) dst[n][8 * g] = decode_word(w[n][g], sc[n][g]);
-      }
+      dst[0] = decode_word(w.x, sc.x);
+      if constexpr (U::NG == 2) dst[8] = decode_word(w.y, sc.y);
     }
   }
 }
