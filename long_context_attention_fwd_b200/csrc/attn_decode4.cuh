@@ -11,9 +11,11 @@
 // than bf16.  At the 24 bytes a clock that an SM gets, turning codes into operands is most of
 // the instructions, so each code is touched once, in registers, and never written back to shared
 // memory: the products are mma.sync m16n8k16 with the codes as the A operand (16 tokens, or 16
-// elements of V, by 16) and the heads of a kv head as the 8-wide N side.  tcgen05 would need the
-// operands as 16-bit values in shared or tensor memory, four times the bytes of the codes, for a
-// product of which a decode step uses 8 columns.
+// elements of V, by 16) and the heads of a kv head as the 8-wide N side.  (A tcgen05 form was
+// built: codes as e4m3 bytes in shared memory, tokens and then elements on the 128-row side, and
+// the heads of q and of the weights in three e4m3 parts each on N.  It was right, and took 271 us
+// where this takes 102: splitting the weights and handing every tile over between warps cost
+// more than the products.)
 //   A nibble needs no conversion: masked out of its word it is the fp16 subnormal code * 2^-24
 //   (or code * 2^-20, the upper nibble of a byte), which the tensor cores multiply exactly; one
 //   AND makes two operands.  The powers of two go into q (K) and into the final scale (V).
@@ -27,10 +29,19 @@
 // Work: the tiles (kTile tokens of one kv head) of all sequences form one line, cut into equal
 // parts, one per block, whatever the lengths.  A block's warps take its tiles in turn; each has
 // its own ring of asynchronous copies, its own reference, sum and output, and waits for nobody.
-// (Copies are 16 bytes a lane: one bulk copy per unit, 2304 bytes, moved 4.3 TB/s at most.)
+// (Copies are 16 bytes a lane: one bulk copy per unit, 2304 bytes, moved 4.3 TB/s at most, where
+// these alone move 6.4.)
 // At the end of a (sequence, kv head) the block's warps join theirs through shared memory; where
 // the pair is shared with other blocks, each writes its part and the last one to finish joins
 // them (done flags with the call's tag, as attn_decode_kernel does).
+//
+// Measured, D = 128, 28 / 4 heads: 48 sequences of 1-32K tokens in pages of 16, 389 MB, 102 us
+// (3.8 TB/s, 58% of the copy rate); one of 32K, 15 us; one of 513, 8 us.  The first is bound by
+// issue: without the copies it takes 81 us, without the products 72, without both 44 (an m16n8k16
+// holds its scheduler's issue for about 7 of its 8 cycles).  The others are latency: the length,
+// the page, the codes and the join are loads behind one another.  Eight warps with 64-token tiles
+// are the best of those tried: more warps need smaller tiles, whose scores, weights and copies
+// overlap less (16 warps of 32 tokens 116 us, two blocks of 8 101 us but 20 us for one of 32K).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -44,12 +55,20 @@ constexpr int kTileUnits = 4;
 constexpr int kTile = kTileUnits * page::kUnit;  // tokens of a tile
 constexpr uint32_t kTopWeight = 0x7400u;         // 2^14 as fp16: a weight this large moves the reference
 constexpr float kFirstWeight = 6.f;              // ... so that the largest becomes 2^6
-constexpr float kSmallStep = 9.313225746154785e-10f;  // 2^-30: smaller steps of V count as this in the reference
+// What else keeps p and p m inside fp32: a token counts in the reference with its steps, 2^-24 of
+// its minima (steps can be 0 where minima are not) and 2^-88 at least, and the reference also
+// moves when p reaches 2^100, or for every tile with a minimum of 2^10 or more.
+constexpr float kMinimumShare = 5.9604644775390625e-8f;
+constexpr float kSmallStep = 3.2311742677852644e-27f;
+constexpr float kTopP = 1.2676506002282294e30f;
+constexpr float kTopMinimum = 1024.f;
+
+constexpr int kMaxParts = 160;                   // blocks that can share a (sequence, kv head)
 
 // NT blocks of 8 heads per pass; a kv head with more than 8 query heads takes passes of 16.
 template <int D, int NT>
 struct Cfg {
-  static constexpr int W = 8;  // warps
+  static constexpr int W = 8;                 // warps
   static constexpr int NS = 2;                // ring stages of a warp
   static constexpr int THREADS = W * 32;
   static constexpr int HEADS = 8 * NT;
@@ -58,7 +77,6 @@ struct Cfg {
   static constexpr int OFF_O = OFF_RING + W * NS * TILE_BYTES;   // [W][HEADS][D] fp32
   static constexpr int OFF_L = OFF_O + W * HEADS * D * 4;        // [W][HEADS] fp32
   static constexpr int OFF_WT = OFF_L + W * HEADS * 4;           // [kMaxParts][HEADS] fp32
-  static constexpr int kMaxParts = 160;                          // blocks that can share an item
   static constexpr int OFF_MISC = OFF_WT + kMaxParts * HEADS * 4;  // merge flag
   static constexpr int SMEM_BYTES = OFF_MISC + 16;
   static_assert(TILE_BYTES % 16 == 0 && SMEM_BYTES <= 227 * 1024, "shared memory");
@@ -467,8 +485,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
         }
       uint32_t pw[TU][NG][NT][2];
       float pr[TU][NT][4];
+      float big = 0.f;   // the largest minimum, in magnitude
+#pragma unroll
+      for (int u = 0; u < TU; ++u)
+#pragma unroll
+        for (int gg = 0; gg < NG; ++gg) big = fmax3(big, fabsf(low_of(vs[u][0][gg])), fabsf(low_of(vs[u][1][gg])));
       auto weigh = [&]() -> bool {
         uint32_t top = 0u;
+        float top_p = 0.f;
 #pragma unroll
         for (int u = 0; u < TU; ++u)
 #pragma unroll
@@ -479,6 +503,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
               const float p1 = ex2_approx(x[u][nt][2 * hh + 1] - ref[nt][1]);
               pr[u][nt][2 * hh] = p0;
               pr[u][nt][2 * hh + 1] = p1;
+              top_p = fmax3(top_p, p0, p1);
 #pragma unroll
               for (int gg = 0; gg < NG; ++gg) {
                 const float s = step_of(vs[u][hh][gg]);
@@ -486,7 +511,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
                 top = max_f16x2(top, pw[u][gg][nt][hh]);
               }
             }
-        return (top & 0xffffu) >= kTopWeight || (top >> 16) >= kTopWeight;
+        return (top & 0xffffu) >= kTopWeight || (top >> 16) >= kTopWeight || top_p >= kTopP || big >= kTopMinimum;
       };
       bool move = first;
       if (!first) move = __any_sync(0xffffffffu, weigh());
@@ -500,8 +525,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
             for (int u = 0; u < TU; ++u)
 #pragma unroll
               for (int hh = 0; hh < 2; ++hh) {
-                float s = fmaxf(step_of(vs[u][hh][0]), kSmallStep);
-                if constexpr (NG == 2) s = fmaxf(s, step_of(vs[u][hh][1]));
+                float s = kSmallStep;
+#pragma unroll
+                for (int gg = 0; gg < NG; ++gg)
+                  s = fmax3(s, step_of(vs[u][hh][gg]), fabsf(low_of(vs[u][hh][gg])) * kMinimumShare);
                 y = fmaxf(y, x[u][nt][2 * hh + e2] + __log2f(s));
               }
 #pragma unroll
@@ -657,7 +684,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
         __threadfence();
         const int parts = c1 - c0 + 1;
         for (int h = warp; h < nh; h += W) {   // the parts' weights, a warp per head
-          constexpr int K = C::kMaxParts / 32;
+          constexpr int K = kMaxParts / 32;
           float y[K], M = -INFINITY, l = 0.f;
 #pragma unroll
           for (int i = 0; i < K; ++i) {
@@ -682,35 +709,17 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
           if (lane == 0) p.lse[row0 + h] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994530942f;
         }
         __syncthreads();
-        // Columns of four elements; the threads left over share a column's parts.
-        const int cols = nh * (D / 4);
-        const int share = W * 32 / cols > 1 ? min(W * 32 / cols, 4) : 1;
-        for (int i0 = 0; i0 < cols; i0 += W * 32) {
-          const int sub = share > 1 ? tid / cols : 0;
-          const int i = share > 1 ? tid % cols : i0 + tid;
-          const int h = i / (D / 4), d4 = i % (D / 4);
+        for (int i = tid; i < nh * (D / 4); i += C::THREADS) {   // columns of four elements
+          const int h = i / (D / 4);
+          const float4* src = reinterpret_cast<const float4*>(p.o_part) + i;
           float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (sub < share && i < cols) {
-            const float4* src = reinterpret_cast<const float4*>(p.o_part) + (long long)h * (D / 4) + d4;
-#pragma unroll 8
-            for (int k = sub; k < parts; k += share) {
-              const float y = s_wt[k * C::HEADS + h];
-              const float4 v = __ldcg(src + (long long)slot_of(c0 + k) * (C::HEADS * (D / 4)));
-              o.x = fmaf(y, v.x, o.x), o.y = fmaf(y, v.y, o.y), o.z = fmaf(y, v.z, o.z), o.w = fmaf(y, v.w, o.w);
-            }
+#pragma unroll 16
+          for (int k = 0; k < parts; ++k) {
+            const float y = s_wt[k * C::HEADS + h];
+            const float4 v = __ldcg(src + (long long)slot_of(c0 + k) * (C::HEADS * (D / 4)));
+            o.x = fmaf(y, v.x, o.x), o.y = fmaf(y, v.y, o.y), o.z = fmaf(y, v.z, o.z), o.w = fmaf(y, v.w, o.w);
           }
-          if (share > 1) {
-            if (sub > 0 && sub < share) reinterpret_cast<float4*>(s_o)[(sub - 1) * cols + i] = o;
-            __syncthreads();
-            if (sub == 0)
-              for (int k = 0; k < share - 1; ++k) {
-                const float4 v = reinterpret_cast<const float4*>(s_o)[k * cols + i];
-                o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
-              }
-          }
-          if (sub == 0 && i < cols)
-            reinterpret_cast<uint2*>(p.o)[(row0 + h) * (D / 4) + d4] =
-                make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+          reinterpret_cast<uint2*>(p.o)[row0 * (D / 4) + i] = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
         }
       }
     }

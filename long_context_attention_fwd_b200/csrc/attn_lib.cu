@@ -504,8 +504,9 @@ Decode4Ws decode4_ws(int B, int Hq, int Hkv, int D, int Lmax) {
   const int G = Hq / Hkv;
   w.nt = G <= 8 ? 1 : 2;
   const int heads = 8 * w.nt;
-  const int warps = w.nt == 1 ? decode4::Cfg<128, 1>::W : decode4::Cfg<128, 2>::W;
-  static_assert(kPlanSMs <= decode4::Cfg<128, 1>::kMaxParts, "blocks that can share an item");
+  constexpr int warps = decode4::Cfg<128, 1>::W;
+  static_assert(warps == decode4::Cfg<128, 2>::W && warps == decode4::Cfg<64, 1>::W, "one plan");
+  static_assert(kPlanSMs <= decode4::kMaxParts, "blocks that can share an item");
   w.passes = (G + heads - 1) / heads;
   w.tiles = (long long)((Lmax + decode4::kTile - 1) / decode4::kTile) * B * Hkv * w.passes;
   w.grid = grid_of((w.tiles + warps - 1) / warps, kPlanSMs);
@@ -801,7 +802,7 @@ attn_status attn_decode(const void* q, const void* k_cache, const void* v_cache,
 
 size_t attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int D, int max_pages, int page_size) {
   int log_ps = 0;
-  if (check_pages(B, max_pages, 1, page_size, &log_ps) != ATTN_OK) return 0;
+  if (Hq > kMaxHeads || check_pages(B, max_pages, 1, page_size, &log_ps) != ATTN_OK) return 0;
   return attn_decode_workspace_size(B, Hq, Hkv, max_pages << log_ps, D);
 }
 
@@ -816,6 +817,7 @@ attn_status attn_decode_paged(const void* q, const void* k_pages, const void* v_
   if (st != ATTN_OK) return st;
   const int Lmax = max_pages << log_ps;
   if ((st = check_decode_sizes(B, Hq, Hkv, Lmax, D, scale)) != ATTN_OK) return st;
+  if (Hq > kMaxHeads) return ATTN_ERR_INVALID_ARG;
   if (!q || !k_pages || !v_pages || !block_table || !cache_len || !o || !lse || !workspace)
     return ATTN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(o, 16) ||
@@ -850,7 +852,7 @@ attn_status attn_decode_paged(const void* q, const void* k_pages, const void* v_
 
 size_t attn_decode_kv4_workspace_size(int B, int Hq, int Hkv, int D, int max_pages, int page_size) {
   int log_ps = 0;
-  if (check_pages(B, max_pages, 1, page_size, &log_ps) != ATTN_OK) return 0;
+  if (Hq > kMaxHeads || check_pages(B, max_pages, 1, page_size, &log_ps) != ATTN_OK) return 0;
   if (check_decode_sizes(B, Hq, Hkv, max_pages << log_ps, D, 1.f) != ATTN_OK) return 0;
   return decode4_ws(B, Hq, Hkv, D, max_pages << log_ps).total;
 }
@@ -865,6 +867,7 @@ attn_status attn_decode_kv4(const void* q, const void* pages, const int32_t* blo
   if (st != ATTN_OK) return st;
   const int Lmax = max_pages << log_ps;
   if ((st = check_decode_sizes(B, Hq, Hkv, Lmax, D, scale)) != ATTN_OK) return st;
+  if (Hq > kMaxHeads) return ATTN_ERR_INVALID_ARG;
   if (!q || !pages || !block_table || !cache_len || !o || !lse || !workspace)
     return ATTN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(pages, 16) || !aligned(o, 16) || !aligned(workspace, 256) ||

@@ -410,6 +410,31 @@ def test_decode_4bit_scales_and_query_sizes(scale, qmult):
     check_decode4(o, lse, q, vals, lens, Hkv, D, float(np.float32(scale)))
 
 
+@pytest.mark.parametrize("kind", ["constant", "huge", "tiny", "mixed", "zero"])
+def test_decode_4bit_values_of_any_size(kind):
+    """V whose groups are constant (steps of 0), near 1e30, near 1e-25, of sizes 2^60 apart from
+    token to token, or all 0, with scores that rise by hundreds after the first tokens."""
+    from long_context_attention_fwd_b200 import ops
+    lens, Hq, Hkv, D, ps = [700, 90], 7, 1, 128, 16
+    rng, q, kv = decode_inputs(lens, Hq, Hkv, D, 29)
+    for b, L in enumerate(lens):
+        k, v = kv[b]
+        ramp = np.linspace(0, 1, L)[:, None, None]
+        k[:] = paged.bf16(k * (1 + 40 * ramp))               # later keys score far higher
+        if kind == "constant":
+            v[:] = paged.bf16(rng.normal(size=(L, Hkv, 1)))
+        elif kind == "zero":
+            v[:] = 0
+        else:
+            size = {"huge": 2.0 ** 100, "tiny": 2.0 ** -80, "mixed": 2.0 ** rng.integers(-30, 31, (L, 1, 1))}[kind]
+            v[:] = paged.bf16(v * size)
+    table, P = paged.table_for(rng, lens, ps)
+    pages, vals = pages4_of(kv, lens, table, P, ps, Hkv, D)
+    o, lse = ops.attn_decode_kv4(to_torch(q), dev(pages), dev(table), dev(np.array(lens, dtype=np.int32)))
+    ok_status()
+    check_decode4(o, lse, q, vals, lens, Hkv, D, 1 / math.sqrt(D))
+
+
 def values_of(table, pages, ps, lens, D):
     out = []
     for b, L in enumerate(lens):
@@ -522,6 +547,61 @@ def test_decode_records_a_page_outside_the_pool(four):
     again, _ = run(fixed)
     ok_status()
     assert torch.equal(good, again)
+
+
+def test_pools_past_32_bits():
+    """Pages whose offsets pass 2^32 bytes (and 2^31 elements): the same tokens as in a small pool
+    are appended to the last pages of large ones, decoded and gathered, to the same bits."""
+    from long_context_attention_fwd_b200 import ops
+    Hq, Hkv, D, ps, n = 8, 4, 128, 64, 300
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    k, v = (torch.randn(n, Hkv, D, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(1, Hq, D, generator=gen, device="cuda").bfloat16()
+    cl, cu = dev(np.array([n], dtype=np.int32)), dev(np.array([0, n], dtype=np.int32))
+    outs = []
+    for P in (5, 130000):                                     # 4.8 GB of 4-bit pages, 8.5 GB of K
+        tb = torch.arange(P - 1, P - 6, -1, dtype=torch.int32, device="cuda")[None].contiguous()
+        pages = ops.kv4_pages(P, ps, Hkv, D)
+        ops.attn_append_kv4(k, v, pages, tb, cl, cu_seqlens=cu)
+        got = [*ops.attn_decode_kv4(q, pages, tb, cl), *ops.attn_gather_kv4(pages, tb, cl, cu, n)]
+        del pages
+        kp, vp = (torch.empty(P, ps, Hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        ops.attn_append_kv(k, v, kp, vp, tb, cl, cu_seqlens=cu)
+        got += [*ops.attn_decode_paged(q, kp, vp, tb, cl), kp[P - 5:].flip(0), vp[P - 5:].flip(0)]
+        got[-2:] = [t.reshape(-1, Hkv, D)[:n].clone() for t in got[-2:]]
+        outs.append(got)
+        del kp, vp
+        torch.cuda.empty_cache()
+    ok_status()
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
+def test_two_decodes_at_once():
+    """Two streams, each with its own workspace, overlapping: the bits of one at a time."""
+    from long_context_attention_fwd_b200 import ops
+    Hq, Hkv, D, ps, L, B = 28, 4, 128, 16, 2000, 6
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    P = B * L // ps
+    table = torch.randperm(P, generator=gen, device="cuda").to(torch.int32).view(B, -1).contiguous()
+    k, v = (torch.randn(B * L, Hkv, D, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    cl = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    pages = ops.kv4_pages(P, ps, Hkv, D)
+    ops.attn_append_kv4(k, v, pages, table, cl, cu_seqlens=torch.arange(0, B * L + 1, L, dtype=torch.int32, device="cuda"))
+    qs = [torch.randn(B, Hq, D, generator=gen, device="cuda").bfloat16() for _ in range(2)]
+    want = [ops.attn_decode_kv4(q, pages, table, cl) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(ops.attn_decode_kv4(qs[i], pages, table, cl))
+    torch.cuda.synchronize()
+    ok_status()
+    for i in range(2):
+        for o, lse in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
 
 
 def test_serving_steps_together():

@@ -61,7 +61,7 @@ def test_decode_refusals_and_workspace(four):
     run = capi.attn_decode_kv4 if four else capi.attn_decode_paged
     assert size(16, 28, 4, 128, 512, 64) > 0
     for bad in [(0, 28, 4, 128, 512, 64), (1, 28, 3, 128, 512, 64), (1, 256, 1, 128, 512, 64),
-                (1, 28, 4, 96, 512, 64), (1, 28, 4, 128, 0, 64), (1, 28, 4, 128, 512, 65),
+                (1, 28, 4, 96, 512, 64), (1, 8192, 8192, 128, 4, 64), (1, 28, 4, 128, 0, 64), (1, 28, 4, 128, 512, 65),
                 (1, 28, 4, 128, 1 << 26, 64)]:
         assert size(*bad) == 0, bad
     need = size(2, 8, 2, 64, 4, 16)
@@ -69,7 +69,7 @@ def test_decode_refusals_and_workspace(four):
               num_pages=9, page_size=16, scale=0.125, workspace=A, workspace_bytes=need, stream=None)
     ok.update(dict(pages=A) if four else dict(k_pages=A, v_pages=A))
     pool = "pages" if four else "k_pages"
-    for change, want in [(dict(B=0), BAD), (dict(Hq=7), BAD), (dict(D=80), UNSUP), (dict(page_size=1), BAD),
+    for change, want in [(dict(B=0), BAD), (dict(Hq=7), BAD), (dict(Hq=8192, Hkv=8192), BAD), (dict(D=80), UNSUP), (dict(page_size=1), BAD),
                          (dict(num_pages=0), BAD), (dict(num_pages=1 << 28), BAD),
                          (dict(scale=float("nan")), BAD), (dict(scale=float("inf")), BAD),
                          (dict(workspace=None), BAD), (dict(workspace_bytes=need - 1), BAD),
