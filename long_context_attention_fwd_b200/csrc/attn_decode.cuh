@@ -106,6 +106,11 @@ enum : unsigned {
   kSiteXFull
 };
 
+// All warps: the softmax warpgroups are back at the launch budget.
+__device__ __forceinline__ void regs_returned() {
+  asm volatile("barrier.cta.sync 2, %0;" ::"n"(kThreads) : "memory");
+}
+
 // Combines the nparts partials of rows row0 .. row0 + G - 1 into p.o and p.lse, with all
 // kThreads threads of the CTA: LSE = ln sum_j exp(LSE_j), O = sum_j exp(LSE_j - LSE) O_j
 // (weights and sums in fp32, one bf16 rounding).  Partials are read through L2 (another
@@ -424,8 +429,12 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       mbar_drain_checked(drain, 0, wc, kSiteDrainMMA);
     }
    }
-   // Back to the launch budget for the merge below, which every warp runs (this waits
-   // for the softmax warpgroups' matching decrease).
+   // Back to the launch budget for the merge below, which every warp runs -- but only once
+   // the softmax warpgroups have given theirs back.  A control warp without work (10, 11, or
+   // all four in a CTA without tiles) that took its registers back at once could do so before
+   // the softmax warps had theirs: these would then wait for registers that nobody frees, and
+   // no time limit ends that wait.
+   regs_returned();
    reg_alloc<kRegsLaunch>();
   } else {
     reg_alloc<kRegsCompute>();
@@ -598,6 +607,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       }
     }
     reg_dealloc<kRegsLaunch>();
+    regs_returned();
   }
 
   // ---- teardown: every role has drained; release tensor memory.
