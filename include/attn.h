@@ -237,8 +237,8 @@ attn_status attn_gather_kv4(const void* pages, const int32_t* block_table, const
                             const int32_t* cu_seqlens, void* k, void* v, int B, int T, int Hkv,
                             int D, int max_pages, int num_pages, int page_size, void* stream);
 
-/* attn_decode over bf16 pages: the same result from the same kernel, each sequence's cache
- * found through block_table.  Lengths are clamped to [0, max_pages * page_size].  A page
+/* attn_decode over bf16 pages, each sequence's cache found through block_table: the same
+ * kernel, with fp32 partial results in the workspace (attn_decode rounds them to bf16).  Lengths are clamped to [0, max_pages * page_size].  A page
  * outside the pool within a sequence's length is recorded and leaves that sequence's o and
  * lse unspecified.  Sizes, workspace rules and determinism as attn_decode. */
 size_t attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int D, int max_pages, int page_size);

@@ -29,7 +29,9 @@
 // PAGED: the cache lies in pages (attn_page.cuh) and a tile is loaded page by page, a box of up
 // to 128 rows each; everything after the loads is the same.  The producer warp's lanes look up
 // the next tile's pages while the current tile's loads wait for room, and each issues its own
-// page's loads.  A page of the table that is not in the pool is recorded and loads zeros.
+// page's loads.  A page of the table that is not in the pool is recorded and loads zeros.  The
+// partial results are fp32 (the dense form's are bf16, one more rounding of 2^-8 each); the
+// weights are bf16 for the product with V, summed as rounded, as in the forward kernel.
 //
 // Each CTA first combines its two streams into one partial (o_s, lse_s).  The last CTA of
 // a (sequence, kv head) to finish then combines the partials of every split into o and
@@ -64,7 +66,7 @@ constexpr int kMaxSplits = 128;  // splits (and partials) per (sequence, kv head
 
 struct Params {
   const int32_t* cache_len;  // [B] (device); clamped to [0, Lmax]
-  __nv_bfloat16* o_part;     // [nsplit][B*Hq][D]: one partial per split
+  void* o_part;              // [nsplit][B*Hq][D]: one partial per split, bf16 (PAGED: fp32)
   float* lse_part;           // [nsplit][B*Hq]
   int Hq, G, Hkv, Lmax;
   int nsplit, tps;           // splits per (sequence, kv head); tiles per split
@@ -113,9 +115,9 @@ __device__ __forceinline__ void regs_returned() {
 
 // Combines the nparts partials of rows row0 .. row0 + G - 1 into p.o and p.lse, with all
 // kThreads threads of the CTA: LSE = ln sum_j exp(LSE_j), O = sum_j exp(LSE_j - LSE) O_j
-// (weights and sums in fp32, one bf16 rounding).  Partials are read through L2 (another
+// (weights and sums in fp32, one bf16 rounding).  F32: the partials' o are fp32.  Partials are read through L2 (another
 // CTA wrote most of them).  `scratch` is shared memory the kernel no longer uses.
-template <int D>
+template <int D, bool F32>
 __device__ void merge_rows(const Params& p, int row0, int G, int nparts, uint8_t* scratch) {
   constexpr int TPR = D / 8;               // threads per row: one 16-byte column group each
   constexpr int NGRP = kThreads / TPR;     // thread groups
@@ -146,18 +148,27 @@ __device__ void merge_rows(const Params& p, int row0, int G, int nparts, uint8_t
   const int rp = G < NGRP ? G : NGRP;
   const int nsub = NGRP / rp;
   const int grp = threadIdx.x / TPR, c = threadIdx.x % TPR;
-  const size_t pstride = size_t(p.rows) * TPR;  // uint4 stride between partials
+  const size_t pstride = size_t(p.rows) * TPR;  // eight columns' stride between partials
   for (int r0 = 0; r0 < G; r0 += rp) {
     const int r = r0 + grp % rp, sub = grp / rp;
     if (sub < nsub && r < G) {
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       const float m = s_m[r];
       if (m != -INFINITY) {
-        const uint4* ob = reinterpret_cast<const uint4*>(p.o_part) + size_t(row0 + r) * TPR + c;
+        const size_t at = size_t(row0 + r) * TPR + c;
         const float* lb = p.lse_part + row0 + r;
 #pragma unroll 4
-        for (int j = sub; j < nparts; j += nsub)
-          merge::acc_bf16x8(acc, __ldcg(ob + size_t(j) * pstride), expf(__ldcg(lb + size_t(j) * p.rows) - m));
+        for (int j = sub; j < nparts; j += nsub) {
+          const float w = expf(__ldcg(lb + size_t(j) * p.rows) - m);
+          if constexpr (F32) {
+            const float4* ob = reinterpret_cast<const float4*>(p.o_part) + 2 * (at + size_t(j) * pstride);
+            const float4 x = __ldcg(ob), y = __ldcg(ob + 1);
+            acc[0] = fmaf(w, x.x, acc[0]), acc[1] = fmaf(w, x.y, acc[1]), acc[2] = fmaf(w, x.z, acc[2]), acc[3] = fmaf(w, x.w, acc[3]);
+            acc[4] = fmaf(w, y.x, acc[4]), acc[5] = fmaf(w, y.y, acc[5]), acc[6] = fmaf(w, y.z, acc[6]), acc[7] = fmaf(w, y.w, acc[7]);
+          } else {
+            merge::acc_bf16x8(acc, __ldcg(reinterpret_cast<const uint4*>(p.o_part) + at + size_t(j) * pstride), w);
+          }
+        }
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) s_acc[(grp * TPR + c) * 8 + e] = acc[e];
@@ -562,15 +573,16 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         ok = __all_sync(0xffffffffu, mbar_wait(x_full, 0, wc, kSiteXFull)) && ok;
         tc_fence_after();
         const bool valid = r < p.G;
-        __nv_bfloat16* orow = p.o_part + (size_t(s) * p.rows + row0 + r) * D;
+        const size_t at = (size_t(s) * p.rows + row0 + r) * D;   // the row's first element
+        uint4* orow = PAGED ? reinterpret_cast<uint4*>(static_cast<float*>(p.o_part) + at)
+                            : reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o_part) + at);
         float* lrow = p.lse_part + size_t(s) * p.rows + row0 + r;
         const float m1 = x_m[r], l1 = x_l[r], lb1 = x_lb[r];
         const float M = fmaxf(m_run, m1);
         if (nt == 0 || M == -INFINITY) {
           if (valid) {
-            uint4* dst = reinterpret_cast<uint4*>(orow);
 #pragma unroll
-            for (int k = 0; k < D / 8; ++k) dst[k] = make_uint4(0u, 0u, 0u, 0u);
+            for (int k = 0; k < (PAGED ? D / 4 : D / 8); ++k) orow[k] = make_uint4(0u, 0u, 0u, 0u);
             *lrow = -INFINITY;
           }
         } else if (ok) {
@@ -594,12 +606,22 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 e0 = fmaf(__uint_as_float(u1[2 * k]), w1, e0);
                 e1 = fmaf(__uint_as_float(u1[2 * k + 1]), w1, e1);
               }
-              pk[k] = pack_bf16x2(e0, e1);
+              if constexpr (PAGED) {
+                u[2 * k] = __float_as_uint(e0);
+                u[2 * k + 1] = __float_as_uint(e1);
+              } else {
+                pk[k] = pack_bf16x2(e0, e1);
+              }
             }
             if (valid) {
-              uint4* dst = reinterpret_cast<uint4*>(orow + ch * 16);
-              dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-              dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+              if constexpr (PAGED) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  orow[ch * 4 + k] = make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
+              } else {
+                orow[ch * 2] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                orow[ch * 2 + 1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+              }
             }
           }
           if (valid) *lrow = (M + __log2f(a0 * l_run + a1 * l1)) * 0.69314718055994530942f;
@@ -637,7 +659,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   __syncthreads();
   if (*s_merge) {
     __threadfence();
-    merge_rows<D>(p, row0, p.G, p.nsplit, smem + C::OFF_K);  // K/V stages are free now
+    merge_rows<D, PAGED>(p, row0, p.G, p.nsplit, smem + C::OFF_K);  // K/V stages are free now
   }
 }
 

@@ -343,13 +343,13 @@ struct DecodeWs {
   size_t o_part, lse_part, flags, total;
   int nsplit, tps, nparts;
 };
-DecodeWs decode_ws(int B, int Hq, int Hkv, int Lmax, int D) {
+DecodeWs decode_ws(int B, int Hq, int Hkv, int Lmax, int D, int part_bytes = 2) {
   DecodeWs w;
   decode_plan(B, Hkv, Lmax, &w.nsplit, &w.tps);
   w.nparts = w.nsplit;  // each split combines its two streams into one partial
   const size_t rows = size_t(B) * Hq;
   w.o_part = 0;
-  w.lse_part = round_up(size_t(w.nparts) * rows * D * 2, 256);
+  w.lse_part = round_up(size_t(w.nparts) * rows * D * part_bytes, 256);
   w.flags = w.lse_part + round_up(size_t(w.nparts) * rows * 4, 256);
   w.total = w.flags + round_up(size_t(B) * Hkv * w.nsplit * 8, 256);
   return w;
@@ -389,7 +389,7 @@ decode::Params decode_params(const DecodeWs& w, const void* q, void* o, float* l
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   decode::Params p{};
   p.cache_len = cache_len;
-  p.o_part = reinterpret_cast<__nv_bfloat16*>(ws + w.o_part);
+  p.o_part = ws + w.o_part;
   p.lse_part = reinterpret_cast<float*>(ws + w.lse_part);
   p.Hq = Hq;
   p.G = Hq / Hkv;
@@ -803,7 +803,8 @@ attn_status attn_decode(const void* q, const void* k_cache, const void* v_cache,
 size_t attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int D, int max_pages, int page_size) {
   int log_ps = 0;
   if (Hq > kMaxHeads || check_pages(B, max_pages, 1, page_size, &log_ps) != ATTN_OK) return 0;
-  return attn_decode_workspace_size(B, Hq, Hkv, max_pages << log_ps, D);
+  if (check_decode_sizes(B, Hq, Hkv, max_pages << log_ps, D, 1.f) != ATTN_OK) return 0;
+  return decode_ws(B, Hq, Hkv, max_pages << log_ps, D, sizeof(float)).total;
 }
 
 attn_status attn_decode_paged(const void* q, const void* k_pages, const void* v_pages,
@@ -824,7 +825,7 @@ attn_status attn_decode_paged(const void* q, const void* k_pages, const void* v_
       !aligned(workspace, 256) || !aligned(lse, 4) || !aligned(cache_len, 4) ||
       !aligned(block_table, 4))
     return ATTN_ERR_MISALIGNED;
-  const DecodeWs w = decode_ws(B, Hq, Hkv, Lmax, D);
+  const DecodeWs w = decode_ws(B, Hq, Hkv, Lmax, D, sizeof(float));
   if (workspace_bytes < w.total) return ATTN_ERR_INVALID_ARG;
   const long long nblocks = (long long)B * Hkv * w.nsplit;
   if (nblocks >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;

@@ -292,8 +292,9 @@ DECODES = [
 
 @pytest.mark.parametrize("case", DECODES, ids=[str(i) for i in range(len(DECODES))])
 def test_decode_paged(case):
-    """Against the fp64 oracle, and bit for bit what attn_decode gives on the dense cache of the
-    same capacity."""
+    """Against the fp64 oracle, and next to what attn_decode gives on the dense cache of the same
+    capacity: the same products and statistics, with partial results that are not rounded to bf16
+    (bit for bit where a sequence is not split)."""
     from long_context_attention_fwd_b200 import ops
     lens, Hq, Hkv, D, ps = case
     rng, q, kv = decode_inputs(lens, Hq, Hkv, D, 21)
@@ -318,8 +319,14 @@ def test_decode_paged(case):
     o, lse = poison((B, Hq, D), torch.bfloat16), poison((B, Hq), torch.float32)
     ops.attn_decode_paged(qt, kp, vp, dev(table), dev(cl), out=o, lse=lse)
     o2, lse2 = ops.attn_decode(qt, kd, vd, dev(cl))
+    vmax = float(np.abs(dense[1]).max())
     ok_status()
-    assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, lse2)
+    assert torch.equal(lse, lse2)
+    # two roundings of the result (to bf16, half a step each) and one of the partials' (2^-8 of P|V|)
+    near = (o.float() - o2.float()).abs() <= 2.0 ** -7 * o2.float().abs() + 2.0 ** -7 * vmax
+    assert bool(near.all())
+    if max(lens) <= 4 * 128:                                  # one split of four tiles
+        assert torch.equal(o.view(torch.int16), o2.view(torch.int16))
     o_r, l_r = oracle.decode(q, dense[0], dense[1], cl, scale)
     oa_r, _ = oracle.decode(q, dense[0], np.abs(dense[1]), cl, scale)
     og, lg = f64(bits_of(o)).reshape(B, Hq, D), lse.double().cpu().numpy()
