@@ -27,9 +27,11 @@
 // product (whatever the cache holds there, 0 * NaN would otherwise poison O).
 //
 // PAGED: the cache lies in pages (attn_page.cuh) and a tile is loaded page by page, a box of up
-// to 128 rows each; everything after the loads is the same.  The producer warp's lanes look up
-// the next tile's pages while the current tile's loads wait for room, and each issues its own
-// page's loads.  A page of the table that is not in the pool is recorded and loads zeros.  The
+// to 128 rows each; everything after the loads is the same.  Warp 8 loads K and warp 10 V; their
+// lanes look up the next tile's pages while the current tile's loads wait for room, and each
+// issues its own page's loads (small boxes are bound by their issue: pages of 16 took 287 us for
+// 16 sequences of 16-32K keys with one issuing lane, 197 with eight, 160 with two warps
+// of eight).  A page of the table that is not in the pool is recorded and loads zeros.  The
 // partial results are fp32 (the dense form's are bf16, one more rounding of 2^-8 each); the
 // weights are bf16 for the product with V, summed as rounded, as in the forward kernel.
 //
@@ -56,6 +58,7 @@ constexpr int BN = 128;
 constexpr int kThreads = 384;
 constexpr int kWarpTMA = 8;
 constexpr int kWarpMMA = 9;
+constexpr int kWarpPagedV = 10;
 constexpr int kRegsLaunch = 168;
 constexpr int kRegsControl = 72;
 constexpr int kRegsCompute = 216;
@@ -273,7 +276,8 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 
   if (warp >= 8) {
    reg_dealloc<kRegsControl>();
-   if (warp == kWarpTMA && n > 0) {
+   const bool is_v = PAGED && warp == kWarpPagedV;   // K and V are loaded by a warp each
+   if ((warp == kWarpTMA || is_v) && n > 0) {
     // ------------------------------------------------------------ producer
     // The last V tile of a sequence whose length is not a tile multiple is loaded on its
     // own barrier, then the whole warp zeroes its rows past the length and hands the
@@ -281,7 +285,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const int n_plain_v = partial_last ? n - 1 : n;
     int nk = 0, nv = 0;
     bool ok = true;
-    if (lane == 0) {
+    if (lane == 0 && !is_v) {
       mbar_arrive_expect_tx(q_full, C::QT_BYTES);
       for (int hf = 0; hf < D / 64; ++hf)
         tma_load_3d(&tm_q, q_full, smem + C::OFF_Q + hf * kSlab, hf * 64, 0, row0);
@@ -317,12 +321,16 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int coord = next;
         const uint32_t bytes = seg_bytes * uint32_t(__popc(__ballot_sync(0xffffffffu, coord >= 0)));
         next = locate(j + 1);
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&k_empty[st], ph ^ 1, wc, kSiteKEmpty)))) break;
-        load(&tm_k, &k_full[st], C::OFF_K, st, coord, bytes);
-        ++nk;
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&v_empty[st], ph ^ 1, wc, kSiteVEmpty)))) break;
-        load(&tm_v, j < n_plain_v ? &v_full[st] : v_raw, C::OFF_V, st, coord, bytes);
-        if (j < n_plain_v) ++nv;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(is_v ? &v_empty[st] : &k_empty[st], ph ^ 1, wc,
+                                                     is_v ? kSiteVEmpty : kSiteKEmpty))))
+          break;
+        if (is_v) {
+          load(&tm_v, j < n_plain_v ? &v_full[st] : v_raw, C::OFF_V, st, coord, bytes);
+          if (j < n_plain_v) ++nv;
+        } else {
+          load(&tm_k, &k_full[st], C::OFF_K, st, coord, bytes);
+          ++nk;
+        }
       }
     } else if (lane == 0) {
       for (int j = 0; j < n && ok; ++j) {
@@ -350,7 +358,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       }
     }
     ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-    if (partial_last) {
+    if (partial_last && is_v == PAGED) {
       const int st = (n - 1) % C::NS;
       // Every lane waits for the raw tile (it was issued unless the loop stopped early).
       bool landed = ok && __all_sync(0xffffffffu, mbar_wait(v_raw, 0, wc, kSiteVRaw));
@@ -378,7 +386,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       // Drain: every issued copy must land before shared memory is released.  Tiles
       // 0..nk-1 (K) and 0..nv-1 (V) completed their stage's barrier in order, so the
       // last phase of stage st is the count of those tiles in that stage, minus one.
-      mbar_drain_checked(q_full, 0, wc, kSiteDrainQ);
+      if (!is_v) mbar_drain_checked(q_full, 0, wc, kSiteDrainQ);
       for (int st = 0; st < C::NS; ++st) {
         const int ck = nk > st ? (nk - 1 - st) / C::NS + 1 : 0;
         const int cv = nv > st ? (nv - 1 - st) / C::NS + 1 : 0;
