@@ -277,14 +277,15 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const Params p) {
 }
 
 // gather4_kernel: packed token t's K and V out of 4-bit pages, x = s * code + m in fp32 (the
-// product is exact: 8 bits by 4), rounded once to bf16.  One warp takes a token; eight threads
+// product is exact: 8 bits by 4), rounded once to bf16.  A warp takes a token, or a share of its
+// rows where tokens are few; eight threads
 // hold a row, each the word (or the two words of both groups) of eight elements, so that reads
 // and writes are whole sectors.  Bound by HBM, by the bf16 rows it writes; with one row a lane in
 // flight 32 registers let all 64 warps of an SM in, which measured faster than three rows and 40.
 struct GatherParams {
   page::PageMap map;
   const uint8_t* pages;
-  int Hkv;
+  int Hkv, share_log;  // 2^share_log warps share a token
   __nv_bfloat16* k;  // [T][Hkv][D]
   __nv_bfloat16* v;
   unsigned* status;
@@ -301,17 +302,19 @@ __device__ __forceinline__ uint4 decode_word(uint32_t w, uint32_t sm) {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 8) gather4_kernel(const GatherParams p) {
   using U = page::Unit<D>;
-  const int warp = (blockIdx.x * kThreads + threadIdx.x) >> 5;
-  const int nwarp = gridDim.x * (kThreads / 32);
+  const long long nwarp = (long long)gridDim.x * (kThreads / 32);
+  const long long items = (long long)p.map.T << p.share_log;
   const int lane = threadIdx.x & 31;
   const int i = lane & 7;                      // words i of each group
   const int rows = 2 * p.Hkv;
-  for (int t = warp; t < p.map.T; t += nwarp) {
+  for (long long item = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); item < items; item += nwarp) {
+    const int t = int(item >> p.share_log);
+    const int first = 4 * (int(item) & ((1 << p.share_log) - 1));
     int pos, pg, slot;
     const page::Placed st = page::place_token(p.map, t, pos, pg, slot);
     if (st == page::kOutside) continue;
     if (st == page::kBad && lane == 0) page::flag_bad_page(p.status, page::kSiteGather);
-    for (int row = lane >> 3; row < rows; row += 4) {
+    for (int row = first + (lane >> 3); row < rows; row += 4 << p.share_log) {
       const bool is_v = row >= p.Hkv;
       const int h = is_v ? row - p.Hkv : row;
       uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v : p.k) + ((long long)t * p.Hkv + h) * D) + i;

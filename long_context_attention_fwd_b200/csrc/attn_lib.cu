@@ -986,7 +986,11 @@ attn_status attn_gather_kv4(const void* pages, const int32_t* block_table, const
   p.k = static_cast<__nv_bfloat16*>(k);
   p.v = static_cast<__nv_bfloat16*>(v);
   p.status = dev->status;
-  const unsigned grid = grid_of((T + append::kThreads / 32 - 1) / (append::kThreads / 32), dev->sms * 8);
+  // A warp per token; where that leaves the SMs' 64 warps idle, more share a token's rows.
+  while (p.share_log < 5 && ((long long)T << (p.share_log + 1)) <= (long long)dev->sms * 64 && (4 << p.share_log) < 2 * Hkv)
+    ++p.share_log;
+  const long long warps = (long long)T << p.share_log;
+  const unsigned grid = grid_of((warps + append::kThreads / 32 - 1) / (append::kThreads / 32), dev->sms * 8);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (D == 64) append::gather4_kernel<64><<<grid, append::kThreads, 0, s>>>(p);
   else append::gather4_kernel<128><<<grid, append::kThreads, 0, s>>>(p);
