@@ -238,9 +238,10 @@ attn_status attn_gather_kv4(const void* pages, const int32_t* block_table, const
                             int D, int max_pages, int num_pages, int page_size, void* stream);
 
 /* attn_decode over bf16 pages, each sequence's cache found through block_table: the same
- * kernel, with fp32 partial results in the workspace (attn_decode rounds them to bf16).  Lengths are clamped to [0, max_pages * page_size].  A page
- * outside the pool within a sequence's length is recorded and leaves that sequence's o and
- * lse unspecified.  Sizes, workspace rules and determinism as attn_decode. */
+ * kernel, with fp32 partial results in the workspace (attn_decode rounds them to bf16).  Lengths
+ * are clamped to [0, max_pages * page_size].  A page outside the pool within a sequence's length
+ * is recorded and leaves that sequence's o and lse unspecified.  Sizes, workspace rules and
+ * determinism as attn_decode. */
 size_t attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int D, int max_pages, int page_size);
 attn_status attn_decode_paged(const void* q, const void* k_pages, const void* v_pages,
                               const int32_t* block_table, const int32_t* cache_len, void* o,
@@ -249,8 +250,9 @@ attn_status attn_decode_paged(const void* q, const void* k_pages, const void* v_
                               size_t workspace_bytes, void* stream);
 
 /* attn_decode over 4-bit pages: the attention over the values the pages stand for.  Codes enter
- * the products as exact integers and scores are summed in fp32; the weights are rounded to bf16
- * for the product with V.  Otherwise as attn_decode_paged (workspace rules included). */
+ * the products as exact integers and scores are summed in fp32; the weights, times V's
+ * steps, are rounded to fp16 for the product with V's codes and summed unrounded.  At most 2^30
+ * tiles of 64 tokens and a kv head (and 16 query heads of it) in the table.  Otherwise as attn_decode_paged (workspace rules included). */
 size_t attn_decode_kv4_workspace_size(int B, int Hq, int Hkv, int D, int max_pages, int page_size);
 attn_status attn_decode_kv4(const void* q, const void* pages, const int32_t* block_table,
                             const int32_t* cache_len, void* o, float* lse, int B, int Hq, int Hkv,

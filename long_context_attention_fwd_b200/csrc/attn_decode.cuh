@@ -65,6 +65,7 @@ constexpr int kRegsCompute = 216;
 static_assert(128 * kRegsControl + 256 * kRegsCompute <= kThreads * kRegsLaunch, "register split");
 constexpr float kRescaleThreshold = 8.0f;
 constexpr int kSlab = 128 * 128;
+constexpr int kSMs = 148;         // SMs a plan is made for
 constexpr int kMaxSplits = 128;  // splits (and partials) per (sequence, kv head)
 
 struct Params {
@@ -195,6 +196,30 @@ __device__ void merge_rows(const Params& p, int row0, int G, int nparts, uint8_t
   }
 }
 
+// Tiles per split of a paged batch, by the rule of the host's plan, but for the lengths as they
+// are: tables are as wide as a sequence may get, and a plan for that width left short sequences
+// to one split each or the SMs to empty ones (one of 32K in a table for 128K: 42 us, now 26, as in
+// a table for 32K; 16 of 2K in tables for 32K: 45 and 28).
+// Four splits an SM, each of four tiles at least; where that is less than two waves, the
+// least that makes one.  Computed by each warp.
+__device__ int batch_tps(const Params& p, int B) {
+  const int lane = threadIdx.x & 31;
+  auto splits = [&](int t) {                             // of the batch
+    int c = 0;
+    for (int i = lane; i < B; i += 32) {
+      const int tiles = (min(max(__ldg(p.cache_len + i), 0), p.Lmax) + BN - 1) / BN;
+      c += (tiles + t - 1) / t;
+    }
+    return (long long)__reduce_add_sync(0xffffffffu, c) * p.Hkv;
+  };
+  const long long total = splits(1);
+  int t = int(max((total + 4 * kSMs - 1) / (4 * kSMs), 4ll));
+  if (splits(t) >= 2 * kSMs) return t;
+  t = int(max((total + kSMs - 1) / kSMs, 4ll));
+  for (int i = 0; i < 16 && splits(t) > kSMs; ++i) t += max(t / 16, 1);
+  return t;
+}
+
 template <int D, bool PAGED = false>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -207,14 +232,21 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   const int lane = threadIdx.x & 31;
 
   // ---- work item: (sequence b, kv head g, split s)
-  const int s = blockIdx.x % p.nsplit;
-  const int bg = blockIdx.x / p.nsplit;
+  const int units = gridDim.x / p.nsplit;                // (sequence, kv head) pairs
+  const int s = PAGED ? blockIdx.x / units : blockIdx.x % p.nsplit;
+  const int bg = PAGED ? blockIdx.x % units : blockIdx.x / p.nsplit;
   const int g = bg % p.Hkv;
   const int b = bg / p.Hkv;
   const int L = min(max(__ldg(p.cache_len + b), 0), p.Lmax);
   const int ntile = (L + BN - 1) / BN;
-  const int j0 = s * p.tps;
-  const int n = max(0, min(ntile - j0, p.tps));         // tiles of this split
+  int tps = p.tps, ns = p.nsplit;                        // tiles per split, splits
+  if constexpr (PAGED) {
+    tps = max(batch_tps(p, units / p.Hkv), (ntile + ns - 1) / ns);
+    ns = max((ntile + tps - 1) / tps, 1);
+    if (s >= ns) return;                                 // no such split: nobody waits for it
+  }
+  const int j0 = s * tps;
+  const int n = max(0, min(ntile - j0, tps));            // tiles of this split
   const int n_t[2] = {(n + 1) >> 1, n >> 1};             // even / odd tiles
   const int last_valid = L - BN * (ntile - 1);           // keys in the sequence's last tile
   const bool partial_last = n > 0 && j0 + n == ntile && last_valid < BN;
@@ -657,17 +689,17 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     __syncwarp();
     __threadfence();  // sequentially consistent: this flag is ordered before the reads below
     bool all = true;
-    for (int i = lane; i < p.nsplit; i += 32) all = all && fl[i] == p.tag;
+    for (int i = lane; i < ns; i += 32) all = all && fl[i] == p.tag;
     all = __all_sync(0xffffffffu, all);
     if (all) {
-      for (int i = lane; i < p.nsplit; i += 32) fl[i] = 0ull;  // a replay starts clean
+      for (int i = lane; i < ns; i += 32) fl[i] = 0ull;  // a replay starts clean
     }
     if (lane == 0) *s_merge = all;
   }
   __syncthreads();
   if (*s_merge) {
     __threadfence();
-    merge_rows<D, PAGED>(p, row0, p.G, p.nsplit, smem + C::OFF_K);  // K/V stages are free now
+    merge_rows<D, PAGED>(p, row0, p.G, ns, smem + C::OFF_K);  // K/V stages are free now
   }
 }
 

@@ -314,7 +314,7 @@ WsLayout ws_layout(int B, int Hq, long long T, int D) {
 // starts at once and no SM waits on a second round.  At most decode_max_splits()
 // partial results.  (Measured on 16 x 16K-32K keys: 140 us with this plan, 161 us with
 // two CTAs per SM; on one 32K sequence: 34 us in one wave, 38 us in 1.7 waves.)
-constexpr int kPlanSMs = 148;
+constexpr int kPlanSMs = decode::kSMs;
 int decode_max_splits() { return decode::kMaxSplits; }
 void decode_plan(int B, int Hkv, int Lmax, int* nsplit, int* tps) {
   const long long ntile = (Lmax + 127) / 128;
@@ -875,7 +875,7 @@ attn_status attn_decode_kv4(const void* q, const void* pages, const int32_t* blo
       !aligned(lse, 4) || !aligned(cache_len, 4) || !aligned(block_table, 4))
     return ATTN_ERR_MISALIGNED;
   const Decode4Ws w = decode4_ws(B, Hq, Hkv, D, Lmax);
-  if (w.tiles >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
+  if (w.tiles >= (1ll << 30)) return ATTN_ERR_INVALID_ARG;
   if (workspace_bytes < w.total) return ATTN_ERR_INVALID_ARG;
   DeviceState* dev = nullptr;
   if ((st = device_setup(&dev, q)) != ATTN_OK) return st;

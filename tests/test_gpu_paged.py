@@ -294,7 +294,8 @@ DECODES = [
 def test_decode_paged(case):
     """Against the fp64 oracle, and next to what attn_decode gives on the dense cache of the same
     capacity: the same products and statistics, with partial results that are not rounded to bf16
-    (bit for bit where a sequence is not split)."""
+    and splits by the lengths in place of the capacity (bit for bit where a sequence is not split:
+    up to four tiles of 128)."""
     from long_context_attention_fwd_b200 import ops
     lens, Hq, Hkv, D, ps = case
     rng, q, kv = decode_inputs(lens, Hq, Hkv, D, 21)
@@ -321,12 +322,17 @@ def test_decode_paged(case):
     o2, lse2 = ops.attn_decode(qt, kd, vd, dev(cl))
     vmax = float(np.abs(dense[1]).max())
     ok_status()
-    assert torch.equal(lse, lse2)
-    # two roundings of the result (to bf16, half a step each) and one of the partials' (2^-8 of P|V|)
+    short = dev(cl) <= 4 * 128
+    assert torch.equal(lse[short], lse2[short])
+    assert torch.equal(o[short].view(torch.int16), o2[short].view(torch.int16))
+    # A weight is rounded to bf16 relative to its own split's maximum, 2^-9 of it either way: sums
+    # with other splits are within 2^-8 of each other, and so are their logarithms.
+    live = dev(cl) > 0
+    assert float((lse - lse2)[live].abs().max()) <= 2.0 ** -8
+    # two roundings of the result (half a step each), one of the partials' and two of the weights'
+    # (2^-9 of P|V| each)
     near = (o.float() - o2.float()).abs() <= 2.0 ** -7 * o2.float().abs() + 2.0 ** -7 * vmax
     assert bool(near.all())
-    if max(lens) <= 4 * 128:                                  # one split of four tiles
-        assert torch.equal(o.view(torch.int16), o2.view(torch.int16))
     o_r, l_r = oracle.decode(q, dense[0], dense[1], cl, scale)
     oa_r, _ = oracle.decode(q, dense[0], np.abs(dense[1]), cl, scale)
     og, lg = f64(bits_of(o)).reshape(B, Hq, D), lse.double().cpu().numpy()
