@@ -204,12 +204,11 @@ __device__ void merge_rows(const Params& p, int row0, int G, int nparts, uint8_t
 // least that makes one.  Computed by each warp.
 __device__ int batch_tps(const Params& p, int B) {
   const int lane = threadIdx.x & 31;
+  auto tiles = [&](int i) { return i < B ? (min(max(__ldg(p.cache_len + i), 0), p.Lmax) + BN - 1) / BN : 0; };
+  const int mine = tiles(lane);
   auto splits = [&](int t) {                             // of the batch
-    int c = 0;
-    for (int i = lane; i < B; i += 32) {
-      const int tiles = (min(max(__ldg(p.cache_len + i), 0), p.Lmax) + BN - 1) / BN;
-      c += (tiles + t - 1) / t;
-    }
+    int c = (mine + t - 1) / t;
+    for (int i = lane + 32; i < B; i += 32) c += (tiles(i) + t - 1) / t;
     return (long long)__reduce_add_sync(0xffffffffu, c) * p.Hkv;
   };
   const long long total = splits(1);

@@ -343,6 +343,43 @@ def test_decode_paged(case):
     assert np.abs(lg[full] - l_r[full]).max() <= TOL_LSE
 
 
+@pytest.mark.parametrize("lens,Hq,Hkv,D,ps,width", [
+    ([int(n) for n in np.random.default_rng(5).integers(0, 600, 40)], 8, 2, 64, 16, 4096),
+    ([20000], 28, 4, 128, 64, 131072), ([9000, 1, 0, 300, 9000], 8, 1, 128, 32, 32768), ([3, 2500], 4, 4, 64, 256, 1 << 20)],
+    ids=["many_short", "one_long", "uneven", "wide"])
+def test_decode_paged_tables_wider_than_the_lengths(lens, Hq, Hkv, D, ps, width):
+    """The splits go by the lengths, whatever the table could hold; the last sequence of an uneven
+    batch has the first one's pages.  Pages behind the lengths do not exist."""
+    from long_context_attention_fwd_b200 import ops
+    shared = len(lens) == 5
+    rng, q, kv = decode_inputs(lens, Hq, Hkv, D, 41)
+    table, P = paged.table_for(rng, lens, ps, width=width // ps)
+    if shared:
+        table[4], kv[4] = table[0], kv[0]
+    kp, vp = poison((P, ps, Hkv, D), torch.bfloat16), poison((P, ps, Hkv, D), torch.bfloat16)
+    dense = np.zeros((2, len(lens), max(lens), Hkv, D))
+    for b, L in enumerate(lens):
+        if L == 0:
+            continue
+        pos = torch.arange(L, device="cuda")
+        pg = dev(table[b])[pos // ps].long()
+        kp[pg, pos % ps], vp[pg, pos % ps] = to_torch(kv[b][0]), to_torch(kv[b][1])
+        dense[:, b, :L] = kv[b]
+    cl = np.array(lens, dtype=np.int32)
+    run = lambda: ops.attn_decode_paged(to_torch(q), kp, vp, dev(table), dev(cl))    # noqa: E731
+    (o, lse), (o2, lse2) = run(), run()
+    ok_status()
+    assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, lse2)
+    o_r, l_r = oracle.decode(q, dense[0], dense[1], cl, 1 / math.sqrt(D))
+    oa_r, _ = oracle.decode(q, dense[0], np.abs(dense[1]), cl, 1 / math.sqrt(D))
+    og, lg = f64(bits_of(o)).reshape(o.shape), lse.double().cpu().numpy()
+    full = cl > 0
+    assert (og[~full] == 0).all() and np.isneginf(lg[~full]).all()
+    rep = o_error_report(og[full], o_r[full], oa_r[full])
+    assert rep["n_over_model"] == 0, rep
+    assert np.abs(lg[full] - l_r[full]).max() <= TOL_LSE
+
+
 def pages4_of(kv, lens, table, P, ps, Hkv, D, fill=255):
     """A pool of 4-bit pages holding the model's rows of kv, the rest `fill`, and the values."""
     pages = np.full((P, Hkv, ps // 16, 18 * D), fill, dtype=np.uint8)
@@ -662,3 +699,54 @@ def test_serving_steps_together():
                 assert float((ll[b] - lf[0, :, -1]).abs().max()) <= 1e-4 + e
             at += n
     ok_status()
+
+
+@pytest.mark.parametrize("four", [False, True])
+def test_captured_step_replayed(four):
+    """One token per sequence appended and attended to, captured once: replays that advance the
+    lengths on the GPU give the bits of the same steps called one by one.  One entry is unused."""
+    from long_context_attention_fwd_b200 import ops
+    start, Hq, Hkv, D, ps, steps = [30, 126, 5], 8, 2, 128, 16, 6
+    B = len(start) + 1
+    rng = np.random.default_rng(17)
+    table, P = paged.table_for(rng, [n + steps for n in start] + [0], ps)
+    tb, rope = dev(table), tuple(dev(t) for t in rope_table(256, D // 2, 9))
+    x = to_torch(paged.bf16(rng.normal(size=(steps, B, Hq + 2 * Hkv, D))))
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    T = sum(start)
+    k0, v0 = (torch.randn(T, Hkv, D, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    one = dev(np.array([1, 1, 1, 0], dtype=np.int32))
+
+    def pools():
+        p = (torch.zeros(P, Hkv, ps // 16, 18 * D, dtype=torch.uint8, device="cuda"),) if four else tuple(
+            torch.zeros(P, ps, Hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        cl = dev(np.array(start + [0], dtype=np.int32))
+        cu = dev(np.concatenate([[0], np.cumsum(start + [0])]).astype(np.int32))
+        (ops.attn_append_kv4 if four else ops.attn_append_kv)(k0, v0, *p, tb, cl, rope=rope, cu_seqlens=cu)
+        return p, cl
+
+    def step(p, cl, cur, q_out):
+        cl.add_(one)
+        q, k, v = cur[:, :Hq], cur[:, Hq:Hq + Hkv], cur[:, Hq + Hkv:]
+        q = (ops.attn_append_kv4 if four else ops.attn_append_kv)(k, v, *p, tb, cl, q=q, rope=rope, q_out=q_out)
+        return (ops.attn_decode_kv4 if four else ops.attn_decode_paged)(q, *p, tb, cl)
+
+    zeros = lambda: torch.zeros(B, Hq, D, dtype=torch.bfloat16, device="cuda")    # noqa: E731
+    p, cl = pools()
+    want = [step(p, cl, x[i], zeros()) for i in range(steps)]
+    pools_want = p
+    p, cl = pools()
+    cur, q_out = x[0].clone(), zeros()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, capture_error_mode="relaxed"):
+        out = step(p, cl, cur, q_out)
+    for i in range(steps):
+        cur.copy_(x[i])
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[0].view(torch.int16), want[i][0].view(torch.int16)) and torch.equal(out[1], want[i][1])
+        assert bool((out[0][3] == 0).all())
+    assert all(torch.equal(a, b) for a, b in zip(p, pools_want))
+    assert cl.tolist() == [n + steps for n in start] + [0]
+    ok_status()
+    del g
