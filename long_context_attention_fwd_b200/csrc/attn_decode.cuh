@@ -240,10 +240,11 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   const int ntile = (L + BN - 1) / BN;
   int tps = p.tps, ns = p.nsplit;                        // tiles per split, splits
   if constexpr (PAGED) {
-    tps = max(batch_tps(p, units / p.Hkv), (ntile + ns - 1) / ns);
+    tps = ns == 1 ? max(ntile, 1) : max(batch_tps(p, units / p.Hkv), (ntile + ns - 1) / ns);
     ns = max((ntile + tps - 1) / tps, 1);
     if (s >= ns) return;                                 // no such split: nobody waits for it
   }
+  const bool whole = PAGED && ns == 1;                   // an only split writes o and lse itself
   const int j0 = s * tps;
   const int n = max(0, min(ntile - j0, tps));            // tiles of this split
   const int n_t[2] = {(n + 1) >> 1, n >> 1};             // even / odd tiles
@@ -613,15 +614,17 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tc_fence_after();
         const bool valid = r < p.G;
         const size_t at = (size_t(s) * p.rows + row0 + r) * D;   // the row's first element
-        uint4* orow = PAGED ? reinterpret_cast<uint4*>(static_cast<float*>(p.o_part) + at)
-                            : reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o_part) + at);
-        float* lrow = p.lse_part + size_t(s) * p.rows + row0 + r;
+        uint4* orow = whole   ? reinterpret_cast<uint4*>(p.o + at)      // s = 0
+                      : PAGED ? reinterpret_cast<uint4*>(static_cast<float*>(p.o_part) + at)
+                              : reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o_part) + at);
+        float* lrow = (whole ? p.lse : p.lse_part + size_t(s) * p.rows) + row0 + r;
         const float m1 = x_m[r], l1 = x_l[r], lb1 = x_lb[r];
         const float M = fmaxf(m_run, m1);
         if (nt == 0 || M == -INFINITY) {
           if (valid) {
 #pragma unroll
-            for (int k = 0; k < (PAGED ? D / 4 : D / 8); ++k) orow[k] = make_uint4(0u, 0u, 0u, 0u);
+            for (int k = 0; k < (PAGED ? D / 4 : D / 8); ++k)
+              if (!whole || k < D / 8) orow[k] = make_uint4(0u, 0u, 0u, 0u);
             *lrow = -INFINITY;
           }
         } else if (ok) {
@@ -648,12 +651,11 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
               if constexpr (PAGED) {
                 u[2 * k] = __float_as_uint(e0);
                 u[2 * k + 1] = __float_as_uint(e1);
-              } else {
-                pk[k] = pack_bf16x2(e0, e1);
               }
+              pk[k] = pack_bf16x2(e0, e1);
             }
             if (valid) {
-              if constexpr (PAGED) {
+              if (PAGED && !whole) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                   orow[ch * 4 + k] = make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
@@ -679,6 +681,8 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
+
+  if (whole) return;
 
   // ---- done flag; the CTA that sees every split of its group done merges the partials.
   volatile int* s_merge = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
