@@ -83,7 +83,7 @@ struct Params {
   unsigned* status;
   unsigned long long timeout_ns;
   const int32_t* table;      // PAGED: [B][width] pages of 2^log_ps tokens; Lmax = width << log_ps
-  int width, num_pages, log_ps;
+  int B, width, num_pages, log_ps;
 };
 
 template <int D>
@@ -196,27 +196,34 @@ __device__ void merge_rows(const Params& p, int row0, int G, int nparts, uint8_t
   }
 }
 
-// Tiles per split of a paged batch, by the rule of the host's plan, but for the lengths as they
-// are: tables are as wide as a sequence may get, and a plan for that width left short sequences
-// to one split each or the SMs to empty ones (one of 32K in a table for 128K: 42 us, now 26, as in
-// a table for 32K; 16 of 2K in tables for 32K: 45 and 28).
-// Four splits an SM, each of four tiles at least; where that is less than two waves, the
-// least that makes one.  Computed by each warp.
-__device__ int batch_tps(const Params& p, int B) {
+// Tiles per split of a sequence of ntile tiles in a paged batch.  Tables are as wide as a sequence
+// may get: the host's plan for that width left short sequences to one split each or the SMs to
+// blocks without work (one of 32K in a table for 128K: 42 us, with this plan 27, as in a table for
+// 32K; 16 of 2K in tables for 32K: 45 and 27).
+// Where splits of four tiles or more make less than two waves of blocks, the least that makes one.
+// Else four splits an SM, of 20 tiles at least, a sequence cut into the nearest number of equal
+// ones: a block's start and its join cost as much as two to four tiles (64 of 1-4K: least of four
+// tiles, cut from the front, 101 us, of 16 81, of 20 76; 100 of 3K: 154 from the front, 119).
+// Computed by each warp, and by reciprocals: it only matters that all blocks find the same.
+__device__ int batch_tps(const Params& p, int ntile) {
   const int lane = threadIdx.x & 31;
-  auto tiles = [&](int i) { return i < B ? (min(max(__ldg(p.cache_len + i), 0), p.Lmax) + BN - 1) / BN : 0; };
-  const int mine = tiles(lane);
-  auto splits = [&](int t) {                             // of the batch
-    int c = (mine + t - 1) / t;
-    for (int i = lane + 32; i < B; i += 32) c += (tiles(i) + t - 1) / t;
-    return (long long)__reduce_add_sync(0xffffffffu, c) * p.Hkv;
+  auto tiles = [&](int i) { return i < p.B ? float((min(max(__ldg(p.cache_len + i), 0), p.Lmax) + BN - 1) / BN) : 0.f; };
+  const float mine = tiles(lane);
+  auto splits = [&](float t) {                           // of the batch, at most 2^30
+    const float inv = 1.f / t;
+    float c = ceilf(fmaf(mine, inv, -1e-4f));
+    for (int i = lane + 32; i < p.B; i += 32) c += ceilf(fmaf(tiles(i), inv, -1e-4f));
+    return float(__reduce_add_sync(0xffffffffu, int(fminf(c, 33554432.f)))) * float(p.Hkv);
   };
-  const long long total = splits(1);
-  int t = int(max((total + 4 * kSMs - 1) / (4 * kSMs), 4ll));
-  if (splits(t) >= 2 * kSMs) return t;
-  t = int(max((total + kSMs - 1) / kSMs, 4ll));
-  for (int i = 0; i < 16 && splits(t) > kSMs; ++i) t += max(t / 16, 1);
-  return t;
+  const float total = splits(1.f);
+  float t = fmaxf(ceilf(total * (0.25f / kSMs)), 20.f);
+  if (splits(t) >= 2 * kSMs) {
+    const int n = max(int(float(ntile) / t + 0.5f), 1);
+    return (ntile + n - 1) / n;
+  }
+  t = fmaxf(ceilf(fmaf(total, 1.f / kSMs, -1e-4f)), 4.f);
+  for (int i = 0; i < 16 && splits(t) > kSMs; ++i) t += fmaxf(floorf(t * 0.0625f), 1.f);
+  return int(t);
 }
 
 template <int D, bool PAGED = false>
@@ -231,7 +238,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   const int lane = threadIdx.x & 31;
 
   // ---- work item: (sequence b, kv head g, split s)
-  const int units = gridDim.x / p.nsplit;                // (sequence, kv head) pairs
+  const int units = p.B * p.Hkv;                         // PAGED: (sequence, kv head) pairs
   const int s = PAGED ? blockIdx.x / units : blockIdx.x % p.nsplit;
   const int bg = PAGED ? blockIdx.x % units : blockIdx.x / p.nsplit;
   const int g = bg % p.Hkv;
@@ -240,7 +247,8 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   const int ntile = (L + BN - 1) / BN;
   int tps = p.tps, ns = p.nsplit;                        // tiles per split, splits
   if constexpr (PAGED) {
-    tps = ns == 1 ? max(ntile, 1) : max(batch_tps(p, units / p.Hkv), (ntile + ns - 1) / ns);
+    tps = ns == 1 ? ntile : max(batch_tps(p, ntile), (ntile + ns - 1) / ns);
+    tps = max(tps, 1);
     ns = max((ntile + tps - 1) / tps, 1);
     if (s >= ns) return;                                 // no such split: nobody waits for it
   }

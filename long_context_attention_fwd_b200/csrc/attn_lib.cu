@@ -839,6 +839,7 @@ attn_status attn_decode_paged(const void* q, const void* k_pages, const void* v_
       make_map(&mv, v_pages, D, Hkv, T, rows))
     return ATTN_ERR_CUDA;
   decode::Params p = decode_params(w, q, o, lse, cache_len, workspace, B, Hq, Hkv, Lmax, scale, *dev);
+  p.B = B;
   p.table = block_table;
   p.width = max_pages;
   p.num_pages = num_pages;
