@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
   // of at most two rounds (joining blocks costs more than a second round).  With few sequences
   // and heads, each begins at a block of its own: a block that ends one and begins the next
   // would be last.
-  int chunk = max((total + int(gridDim.x) - 1) / int(gridDim.x), W);
-  if (chunk < 4 * W) chunk = (chunk + W - 1) / W * W;
+  int chunk = max((total + int(gridDim.x) - 1) / int(gridDim.x), min(W, longest));
+  if (longest > W && chunk < 4 * W) chunk = (chunk + W - 1) / W * W;
   if (longest <= 2 * W) chunk = max(chunk, longest);
   const bool apart = p.B <= 32 && 4 * p.B * nv <= int(gridDim.x);
   if (apart) {

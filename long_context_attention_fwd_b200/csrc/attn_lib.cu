@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <chrono>
 #include <unistd.h>
@@ -509,7 +510,7 @@ Decode4Ws decode4_ws(int B, int Hq, int Hkv, int D, int Lmax) {
   static_assert(kPlanSMs <= decode4::kMaxParts, "blocks that can share an item");
   w.passes = (G + heads - 1) / heads;
   w.tiles = (long long)((Lmax + decode4::kTile - 1) / decode4::kTile) * B * Hkv * w.passes;
-  w.grid = grid_of((w.tiles + warps - 1) / warps, kPlanSMs);
+  w.grid = grid_of(std::max((w.tiles + warps - 1) / warps, (long long)B * Hkv * w.passes), kPlanSMs);
   const size_t parts = 2 * size_t(w.grid) * heads;
   w.l_part = round_up(parts * D * sizeof(float), 256);
   w.flags = w.l_part + round_up(parts * sizeof(float), 256);
