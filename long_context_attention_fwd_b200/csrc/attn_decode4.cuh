@@ -138,21 +138,25 @@ __device__ __forceinline__ int length_of(const Params& p, int b) {
 }
 __device__ __forceinline__ int tiles_of(int L) { return (L + kTile - 1) / kTile; }
 
-// Place on the line of tiles: tile j of the nt tiles of (sequence b, head block vh).
+// Place on the line of tiles: tile j of the nt tiles of (sequence b, head block vh).  settle: on to
+// the item that j, past the end, lies in; returns the items passed.
 struct Cursor {
   int b, vh, j, nt, L;
-  __device__ __forceinline__ void settle(const Params& p, int nv) {
+  __device__ __forceinline__ int settle(const Params& p, int nv) {
+    int passed = 0;
     while (j >= nt) {
       j -= nt;
+      ++passed;
       if (++vh == nv) {
         vh = 0;
         do {
-          if (++b >= p.B) return;  // past the end of the line
+          if (++b >= p.B) return passed;  // past the end of the line
           L = length_of(p, b);
           nt = tiles_of(L);
         } while (nt == 0);
       }
     }
+    return passed;
   }
 };
 
@@ -173,26 +177,38 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
   const int nv = p.Hkv * p.RB;
 
   // ---- this block's part [t0, t1) of the line, and where it starts (every warp by itself)
-  int total = 0, longest = 0;
+  int total = 0, longest = 0, live = 0;
   for (int b = lane; b < p.B; b += 32) {
     const int n = tiles_of(length_of(p, b));
     total += n;
+    live += n > 0;
     longest = max(longest, n);
   }
   total = __reduce_add_sync(0xffffffffu, total) * nv;
+  live = __reduce_add_sync(0xffffffffu, live) * nv;
   longest = __reduce_max_sync(0xffffffffu, longest);
-  // Equal parts.  While they are short: whole rounds of the warps, and no cut through sequences
-  // of at most two rounds (joining blocks costs more than a second round).  With few sequences
-  // and heads, each begins at a block of its own: a block that ends one and begins the next
-  // would be last.
-  int chunk = max((total + int(gridDim.x) - 1) / int(gridDim.x), min(W, longest));
-  if (longest > W && chunk < 4 * W) chunk = (chunk + W - 1) / W * W;
-  if (longest <= 2 * W) chunk = max(chunk, longest);
-  const bool apart = p.B <= 32 && 4 * p.B * nv <= int(gridDim.x);
+  const int grid = int(gridDim.x);
+  auto share = [&] {
+    // Equal parts.  While they are short: whole rounds of the warps, and no cut through sequences
+    // of at most two rounds (joining blocks costs more than a second round).
+    int x = max((total + grid - 1) / grid, min(W, longest));
+    if (longest > W && x < 4 * W) x = (x + W - 1) / W * W;
+    return longest <= 2 * W ? max(x, longest) : x;
+  };
+  // With few sequences and heads, each begins at a block of its own: a block that ends one and
+  // begins the next would be last.  Otherwise every item has W places without tiles behind it on
+  // the line, what its start and its join cost (64 sequences of 1-600 tokens: 55 us without
+  // them, 19 with them).
+  int chunk = share();
+  const bool apart = p.B <= 32 && 4 * p.B * nv <= grid;
   if (apart) {
     const int n = lane < p.B ? tiles_of(length_of(p, lane)) : 0;
-    while (int(__reduce_add_sync(0xffffffffu, (n + chunk - 1) / chunk)) * nv > int(gridDim.x)) chunk += max(W, chunk / 16);
+    while (int(__reduce_add_sync(0xffffffffu, (n + chunk - 1) / chunk)) * nv > grid) chunk += max(W, chunk / 16);
     total = __reduce_add_sync(0xffffffffu, (n + chunk - 1) / chunk) * nv * chunk;
+  } else {
+    total += live * W;
+    chunk = share();
+    if (longest <= 2 * W) chunk = max(chunk, longest + W);
   }
   const int t0 = min(total, int(blockIdx.x) * chunk);
   int t1 = min(total, t0 + chunk);
@@ -206,10 +222,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
       }
   if (t0 >= t1) return;
 
-  Cursor item;  // the (sequence, head block) the block is at; j counts from the item's own start
+  int start = t0;  // the block's first tile
+  Cursor item;     // the (sequence, head block) the block is at; j counts from the item's own start
   for (int b0 = 0, before = 0;; b0 += 32) {
     const int L = b0 + lane < p.B ? length_of(p, b0 + lane) : 0;
-    const int own = apart ? (tiles_of(L) + chunk - 1) / chunk * chunk : tiles_of(L);  // of the line, per head
+    const int nt = tiles_of(L);                         // own: places on the line, per head
+    const int own = apart ? (nt + chunk - 1) / chunk * chunk : nt > 0 ? nt + W : 0;
     const int n = own * nv;
     int incl = n;
 #pragma unroll
@@ -228,19 +246,27 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
       item.vh = off / each;
       item.j = off % each;
       if (apart) t1 = min(t1, t0 + item.nt - item.j);
+      if (item.j >= item.nt) {                           // behind the item's tiles: on to the next
+        start += each - item.j;
+        item.j = item.nt;
+        if (start < t1) item.settle(p, nv);
+      }
       break;
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
   }
 
-  // ---- this warp's copies: tiles t0 + warp, t0 + warp + W, ...
+  if (start >= t1) return;
+
+  // ---- this warp's copies: tiles start + warp, start + warp + W, ...; the W places behind an item
+  // keep the warps' turns as they are
   uint8_t* ring = smem + C::OFF_RING + warp * C::NS * C::TILE_BYTES;
   const uint32_t ring_lane = smem_u32(ring) + lane * 16;
   const int upp_log = p.log_ps - 4;                     // units of a page
   const long long page_bytes = ((long long)p.Hkv << upp_log) * U::BYTES;
   Cursor next = item;
   next.j += warp;
-  int t_next = t0 + warp;
+  int t_next = start + warp;
   int pg[TU] = {};                                      // pages of the next tile's units
   auto fetch_pages = [&] {
     const int32_t* row = p.table + (long long)next.b * p.width;
@@ -278,22 +304,22 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
       t_next += W;
       next.j += W;
       if (t_next < t1) {
-        next.settle(p, nv);
-        fetch_pages();
+        t_next += W * next.settle(p, nv);
+        if (t_next < t1) fetch_pages();
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   if (t_next < t1) {
-    next.settle(p, nv);
-    fetch_pages();
+    t_next += W * next.settle(p, nv);
+    if (t_next < t1) fetch_pages();
   }
 #pragma unroll
   for (int i = 0; i < C::NS; ++i) issue(i);
 
   // ---- tiles
   int st = 0;                  // ring stage of this warp's next tile
-  int t = t0, tw = t0 + warp;  // start of the item's part on the line; this warp's next tile
+  int t = start, tw = start + warp;  // start of the item's part on the line; this warp's next tile
   const int key0 = token_of(r);
   while (t < t1) {
     const int e = min(t1, t + item.nt - item.j);         // end of the item's part
@@ -633,7 +659,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
     const int slot = 2 * blockIdx.x + (a_line < t0 ? 0 : 1);
     const long long row0 = (long long)item.b * p.Hq + h0;
     const int nw = min(W, e - t);                               // warps that had a tile
-    const int w0 = (t - t0) % W;                                // the first of them
+    const int w0 = (t - start) % W;                                // the first of them
     for (int i = tid; i < nh * (D / 4); i += W * 32) {
       const int h = i / (D / 4), d4 = i % (D / 4);
       float M = -INFINITY;
@@ -727,7 +753,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
 
     item.j += e - t;
     t = e;
-    if (t < t1) item.settle(p, nv);
+    if (t < t1) {
+      item.settle(p, nv);
+      t += W;
+      tw += W;
+    }
   }
 }
 

@@ -496,7 +496,7 @@ unsigned append_grid(append::Params* p, int D, unsigned sms) {
 // of 16.  The workspace holds two shared parts per block.
 struct Decode4Ws {
   size_t l_part, flags, total;
-  long long tiles;
+  long long tiles, line;  // at most: tiles, and with the places behind each item
   int nt, passes;
   unsigned grid;
 };
@@ -510,7 +510,9 @@ Decode4Ws decode4_ws(int B, int Hq, int Hkv, int D, int Lmax) {
   static_assert(kPlanSMs <= decode4::kMaxParts, "blocks that can share an item");
   w.passes = (G + heads - 1) / heads;
   w.tiles = (long long)((Lmax + decode4::kTile - 1) / decode4::kTile) * B * Hkv * w.passes;
-  w.grid = grid_of(std::max((w.tiles + warps - 1) / warps, (long long)B * Hkv * w.passes), kPlanSMs);
+  const long long items = (long long)B * Hkv * w.passes;
+  w.grid = grid_of(std::max((w.tiles + warps - 1) / warps, items), kPlanSMs);
+  w.line = w.tiles + warps * items;
   const size_t parts = 2 * size_t(w.grid) * heads;
   w.l_part = round_up(parts * D * sizeof(float), 256);
   w.flags = w.l_part + round_up(parts * sizeof(float), 256);
@@ -877,7 +879,7 @@ attn_status attn_decode_kv4(const void* q, const void* pages, const int32_t* blo
       !aligned(lse, 4) || !aligned(cache_len, 4) || !aligned(block_table, 4))
     return ATTN_ERR_MISALIGNED;
   const Decode4Ws w = decode4_ws(B, Hq, Hkv, D, Lmax);
-  if (w.tiles >= (1ll << 30)) return ATTN_ERR_INVALID_ARG;
+  if (w.line >= (1ll << 30)) return ATTN_ERR_INVALID_ARG;
   if (workspace_bytes < w.total) return ATTN_ERR_INVALID_ARG;
   DeviceState* dev = nullptr;
   if ((st = device_setup(&dev, q)) != ATTN_OK) return st;
