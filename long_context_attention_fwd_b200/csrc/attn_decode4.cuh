@@ -195,12 +195,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
     if (longest > W && x < 4 * W) x = (x + W - 1) / W * W;
     return longest <= 2 * W ? max(x, longest) : x;
   };
-  // With few sequences and heads, each begins at a block of its own: a block that ends one and
-  // begins the next would be last.  Otherwise every item has W places without tiles behind it on
+  // With few sequences and heads, or short ones and a block for each, each begins at a block of its
+  // own: a block that ends one and begins the next would be last.  Otherwise every item has W places without tiles behind it on
   // the line, what its start and its join cost (64 sequences of 1-600 tokens: 55 us without
   // them, 19 with them).
   int chunk = share();
-  const bool apart = p.B <= 32 && 4 * p.B * nv <= grid;
+  const bool apart = p.B <= 32 && (4 * p.B * nv <= grid || (longest <= 2 * W && live <= grid));
   if (apart) {
     const int n = lane < p.B ? tiles_of(length_of(p, lane)) : 0;
     while (int(__reduce_add_sync(0xffffffffu, (n + chunk - 1) / chunk)) * nv > grid) chunk += max(W, chunk / 16);

@@ -511,7 +511,7 @@ Decode4Ws decode4_ws(int B, int Hq, int Hkv, int D, int Lmax) {
   w.passes = (G + heads - 1) / heads;
   w.tiles = (long long)((Lmax + decode4::kTile - 1) / decode4::kTile) * B * Hkv * w.passes;
   const long long items = (long long)B * Hkv * w.passes;
-  w.grid = grid_of(std::max((w.tiles + warps - 1) / warps, items), kPlanSMs);
+  w.grid = grid_of(std::max((w.tiles + warps - 1) / warps, 4 * items), kPlanSMs);
   w.line = w.tiles + warps * items;
   const size_t parts = 2 * size_t(w.grid) * heads;
   w.l_part = round_up(parts * D * sizeof(float), 256);
