@@ -26,8 +26,8 @@
 //      R_h, which is not the largest score but moves so that p s, p = 2^(x - R), stays below 2^14
 //      and its largest value so far is at least 1; sums of p and of p m are fp32.
 //
-// Work: the tiles (kTile tokens of one kv head) of all sequences form one line, cut into equal
-// parts, one per block, whatever the lengths.  A block's warps take its tiles in turn; each has
+// Work: the tiles (kTile tokens of one kv head) of all sequences form one line, with empty places
+// for each start, cut into equal parts, one per block, whatever the lengths.  A block's warps take its tiles in turn; each has
 // its own ring of asynchronous copies, its own reference, sum and output, and waits for nobody.
 // (Copies are 16 bytes a lane: one bulk copy per unit, 2304 bytes, moved 4.3 TB/s at most, where
 // these alone move 6.4.)
@@ -35,10 +35,10 @@
 // the pair is shared with other blocks, each writes its part and the last one to finish joins
 // them (done flags with the call's tag, as attn_decode_kernel does).
 //
-// Measured, D = 128, 28 / 4 heads: 48 sequences of 1-32K tokens in pages of 16, 389 MB, 102 us
-// (3.8 TB/s, 58% of the copy rate); one of 32K, 15 us; one of 513, 8 us.  The first is bound by
-// issue: without the copies it takes 81 us, without the products 72, without both 44 (an m16n8k16
-// holds its scheduler's issue for about 7 of its 8 cycles).  The others are latency: the length,
+// Measured, D = 128, 28 / 4 heads: 48 sequences of 1-32K tokens in pages of 16, 389 MB, 98 us
+// (4.0 TB/s, 61% of the copy rate); one of 32K, 15 us; one of 513, 9 us.  The first is bound by
+// issue (when it took 102 us: without the copies 81, without the products 72, without both 44; an
+// m16n8k16 holds its scheduler's issue for about 7 of its 8 cycles).  The others are latency: the length,
 // the page, the codes and the join are loads behind one another.  Eight warps with 64-token tiles
 // are the best of those tried: more warps need smaller tiles, whose scores, weights and copies
 // overlap less (16 warps of 32 tokens 116 us, two blocks of 8 101 us but 20 us for one of 32K).

@@ -491,8 +491,8 @@ unsigned append_grid(append::Params* p, int D, unsigned sms) {
   return grid_of((warps + per_block - 1) / per_block, sms * 8);
 }
 
-// Plan of the 4-bit decode: one block per SM, fewer where the longest possible batch has no
-// tile for every warp.  Up to 8 query heads of a kv head take one pass of 8, more take passes
+// Plan of the 4-bit decode: one block per SM, fewer where the longest possible batch has
+// neither a tile for every warp nor a (sequence, kv head) for every fourth block.  Up to 8 query heads of a kv head take one pass of 8, more take passes
 // of 16.  The workspace holds two shared parts per block.
 struct Decode4Ws {
   size_t l_part, flags, total;

@@ -485,6 +485,23 @@ def test_decode_4bit_values_of_any_size(kind):
     check_decode4(o, lse, q, vals, lens, Hkv, D, 1 / math.sqrt(D))
 
 
+@pytest.mark.parametrize("lens,Hq,Hkv,D,ps", [
+    ([int(n) for n in np.random.default_rng(6).integers(0, 600, 64)], 8, 2, 64, 16),
+    ([1] * 70, 4, 4, 64, 32), ([852, 1], 40, 40, 128, 32), ([1, 500, 200], 32, 4, 128, 64),
+    ([64 * i for i in range(33)], 4, 1, 64, 64), ([3000, 0, 1, 1, 0, 65, 1100] * 6, 20, 1, 128, 128)],
+    ids=["ragged", "ones", "many_heads", "few", "full_tiles", "long_and_short"])
+def test_decode_4bit_many_short(lens, Hq, Hkv, D, ps):
+    """Several sequences and heads in a block, cut anywhere; tables also wider than the lengths."""
+    from long_context_attention_fwd_b200 import ops
+    rng, q, kv = decode_inputs(lens, Hq, Hkv, D, 33)
+    for width in (None, 8192 // ps):
+        table, P = paged.table_for(rng, lens, ps, width=width)
+        pages, vals = pages4_of(kv, lens, table, P, ps, Hkv, D)
+        o, lse = ops.attn_decode_kv4(to_torch(q), dev(pages), dev(table), dev(np.array(lens, dtype=np.int32)))
+        ok_status()
+        check_decode4(o, lse, q, vals, lens, Hkv, D, 1 / math.sqrt(D))
+
+
 def values_of(table, pages, ps, lens, D):
     out = []
     for b, L in enumerate(lens):
