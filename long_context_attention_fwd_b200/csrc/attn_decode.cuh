@@ -65,6 +65,7 @@ constexpr int kRegsCompute = 216;
 static_assert(128 * kRegsControl + 256 * kRegsCompute <= kThreads * kRegsLaunch, "register split");
 constexpr float kRescaleThreshold = 8.0f;
 constexpr int kSlab = 128 * 128;
+constexpr uint32_t kNegateA = 1u << 13;  // of the product's instruction descriptor
 constexpr int kSMs = 148;         // SMs a plan is made for
 constexpr int kMaxSplits = 128;  // splits (and partials) per (sequence, kv head)
 
@@ -79,7 +80,8 @@ struct Params {
   unsigned long long tag;    // this call's tag (nonzero)
   __nv_bfloat16* o;          // [B * Hq][D] result
   float* lse;                // [B * Hq]
-  float scale_log2;
+  float scale_log2;          // |scale| log2(e), above 0: a masked score of -inf stays so
+  int negate;                // scale < 0: the first product takes -q
   unsigned* status;
   unsigned long long timeout_ns;
   const int32_t* table;      // PAGED: [B][width] pages of 2^log_ps tokens; Lmax = width << log_ps
@@ -437,7 +439,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
    } else if (warp == kWarpMMA && n > 0) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      constexpr uint32_t idS = idesc_bf16_f32(128, 128, 0, 0);
+      const uint32_t idS = idesc_bf16_f32(128, 128, 0, 0) | (p.negate ? kNegateA : 0u);
       constexpr uint32_t idPV = idesc_bf16_f32(128, D, 0, 1);
       const uint32_t qb = smem_u32(smem + C::OFF_Q);
       const uint32_t colS[2] = {C::COL_S0, C::COL_S1};

@@ -8,6 +8,7 @@
 #include <atomic>
 #include <chrono>
 #include <unistd.h>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
@@ -403,7 +404,9 @@ decode::Params decode_params(const DecodeWs& w, const void* q, void* o, float* l
   p.tag = next_decode_tag();
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  // Scale 0 becomes the smallest normal number, next to which scores below 2^100 vanish.
+  p.scale_log2 = std::max(std::fabs(scale) * 1.4426950408889634f, FLT_MIN);
+  p.negate = scale < 0.f;
   p.status = dev.status;
   p.timeout_ns = g_timeout_ns.load();
   return p;
