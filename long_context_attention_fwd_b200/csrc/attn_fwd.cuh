@@ -59,6 +59,7 @@ constexpr int kRegsLaunch = 168;
 constexpr int kRegsControl = 88;
 constexpr int kRegsCompute = 208;
 static_assert(128 * kRegsControl + 256 * kRegsCompute <= kThreads * kRegsLaunch, "register split");
+constexpr uint32_t kNegateA = 1u << 13;    // of the product's instruction descriptor
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O when max grows > 2^8
 constexpr int kSlab = 128 * 128;       // one 128-row x 64-column bf16 swizzled slab (16 KB)
 // Share of the exponentials (pairs out of 16) computed on the FMA pipe, per head dim.
@@ -100,7 +101,8 @@ struct Params {
   float* lse;
   int Hq, G, T;                        // query heads, query heads per kv head, total tokens
   int causal;
-  float scale_log2;                    // softmax scale * log2(e) (* q, k descale for e4m3)
+  float scale_log2;                    // |softmax scale| * log2(e) (* q, k descale for e4m3), above 0
+  int negate;                          // the scale is negative: the first product takes -q
   float o_scale;                       // 1, or the v descale for e4m3
   int nblk;                            // (T >> 8) + nseq: upper bound of 256-row blocks
   int nitems;                          // nblk * Hq work items
@@ -343,7 +345,9 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
    } else if (warp == kWarpMMA) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      constexpr uint32_t idS = FP8 ? idesc_e4m3_f32(128, 128, 0, 0) : idesc_bf16_f32(128, 128, 0, 0);
+      // Masked scores are -inf before they are scaled, so the factor must be positive.
+      const uint32_t idS = (FP8 ? idesc_e4m3_f32(128, 128, 0, 0) : idesc_bf16_f32(128, 128, 0, 0)) |
+                           (p.negate ? kNegateA : 0u);
       constexpr uint32_t idPV = FP8 ? idesc_e4m3_f32(128, D, 0, 1) : idesc_bf16_f32(128, C::NPV, 0, 1);
       const uint32_t qb[2] = {smem_u32(smem + C::OFF_Q), smem_u32(smem + C::OFF_Q + C::QT_BYTES)};
       const uint32_t colS[2] = {C::COL_S0, C::COL_S1};

@@ -280,6 +280,10 @@ attn_status check_sizes(int B, int Hq, int Hkv, int S, int D, float scale, bool 
   return ATTN_OK;
 }
 
+// |scale| log2(e) for the kernels that mask scores before they scale them.  Scale 0 becomes the
+// smallest normal number, by which scores below 2^100 vanish and a masked -inf does not.
+float positive_log2(float scale) { return std::max(std::fabs(scale) * 1.4426950408889634f, FLT_MIN); }
+
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Grid of the forward kernel.  Dense batches at D = 128: persistent, one CTA per SM (its
@@ -404,8 +408,7 @@ decode::Params decode_params(const DecodeWs& w, const void* q, void* o, float* l
   p.tag = next_decode_tag();
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
-  // Scale 0 becomes the smallest normal number, next to which scores below 2^100 vanish.
-  p.scale_log2 = std::max(std::fabs(scale) * 1.4426950408889634f, FLT_MIN);
+  p.scale_log2 = positive_log2(scale);
   p.negate = scale < 0.f;
   p.status = dev.status;
   p.timeout_ns = g_timeout_ns.load();
@@ -578,7 +581,8 @@ attn_status attn_fwd(const void* q, const void* k, const void* v, void* o, float
   p.G = Hq / Hkv;
   p.T = int(T);
   p.causal = causal ? 1 : 0;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = positive_log2(scale);
+  p.negate = scale < 0.f;
   p.o_scale = 1.f;
   p.nblk = int((T >> 8) + B);
   p.nitems = p.nblk * Hq;
@@ -622,7 +626,8 @@ attn_status attn_fwd_fp8(const void* q, const void* k, const void* v, void* o, f
   p.G = Hq / Hkv;
   p.T = int(T);
   p.causal = causal ? 1 : 0;
-  p.scale_log2 = scale * q_descale * k_descale * 1.4426950408889634f;
+  p.scale_log2 = positive_log2(scale * q_descale * k_descale);
+  p.negate = scale * q_descale * k_descale < 0.f;
   p.o_scale = v_descale;
   p.nblk = int((T >> 8) + B);
   p.nitems = p.nblk * Hq;
