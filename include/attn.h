@@ -239,7 +239,8 @@ attn_status attn_gather_kv4(const void* pages, const int32_t* block_table, const
 
 /* attn_decode over bf16 pages, each sequence's cache found through block_table: the same
  * kernel, with fp32 partial results in the workspace (attn_decode rounds them to bf16).  Lengths
- * are clamped to [0, max_pages * page_size].  A page outside the pool within a sequence's length
+ * are clamped to [0, max_pages * page_size]; one above that is recorded, and its sequence attends
+ * to the tokens that its table holds.  A page outside the pool within a sequence's length
  * is recorded and leaves that sequence's o and lse unspecified.  Sizes, workspace rules and
  * determinism as attn_decode. */
 size_t attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int D, int max_pages, int page_size);

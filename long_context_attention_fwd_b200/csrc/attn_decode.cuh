@@ -245,8 +245,11 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   const int bg = PAGED ? blockIdx.x % units : blockIdx.x / p.nsplit;
   const int g = bg % p.Hkv;
   const int b = bg / p.Hkv;
-  const int L = min(max(__ldg(p.cache_len + b), 0), p.Lmax);
+  const int length = __ldg(p.cache_len + b);
+  const int L = min(max(length, 0), p.Lmax);
   const int ntile = (L + BN - 1) / BN;
+  if (PAGED && s == 0 && g == 0 && threadIdx.x == 0 && length > p.Lmax)
+    page::flag_bad_page(p.status, page::kSiteDecode);
   int tps = p.tps, ns = p.nsplit;                        // tiles per split, splits
   if constexpr (PAGED) {
     tps = ns == 1 ? ntile : max(batch_tps(p, ntile), (ntile + ns - 1) / ns);

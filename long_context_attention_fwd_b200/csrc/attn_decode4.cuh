@@ -213,13 +213,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
   const int t0 = min(total, int(blockIdx.x) * chunk);
   int t1 = min(total, t0 + chunk);
 
-  // Sequences without tokens: o = 0, lse = -inf.
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+  // Sequences without tokens: o = 0, lse = -inf.  Lengths that the table has no pages for are recorded.
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (tid == 0 && __ldg(p.cache_len + b) > p.width << p.log_ps) page::flag_bad_page(p.status, page::kSiteDecode4);
     if (length_of(p, b) == 0)
       for (int i = tid; i < p.Hq * (D / 8); i += C::THREADS) {
         reinterpret_cast<uint4*>(p.o)[(long long)b * p.Hq * (D / 8) + i] = make_uint4(0u, 0u, 0u, 0u);
         if (i < p.Hq) p.lse[(long long)b * p.Hq + i] = -INFINITY;
       }
+  }
   if (t0 >= t1) return;
 
   int start = t0;  // the block's first tile

@@ -525,7 +525,8 @@ def attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Ten
     block_table int32 [B, max_pages], cache_len int32 [B].  Returns (o [B, Hq, D] bf16, lse
     [B, Hq] fp32); a sequence of length 0 gets o = 0 and lse = -inf.  Table entries past a
     sequence's length are not read; one within it that is not in the pool is reported by
-    attn_device_status and leaves that sequence's result unspecified."""
+    attn_device_status and leaves that sequence's result unspecified.  A length that the table has
+    no pages for is reported too, and the sequence attends to the tokens that the table holds."""
     P, Hkv, ps, D = _check_paged(k_pages, v_pages)
     dev = k_pages.device
     scale, out, lse, workspace, nbytes, B, Hq, width = _decode_args(

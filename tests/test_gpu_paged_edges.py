@@ -1,0 +1,48 @@
+"""Paged caches on the GPU at the edges of what their documentation allows."""
+import math
+
+import numpy as np
+import pytest
+
+import paged
+from helpers import bits_of, f64
+from test_gpu_paged import (check_decode4, decode_inputs, dev, ok_status, pages4_of, poison, rope_table,
+                            status, to_torch, values_of)
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def same(a, b):
+    return torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("lens", [[20, 33, 7], [1 << 30, 31], [33], [20] * 40 + [1000]])
+def test_decode_records_a_length_past_the_table(four, lens):
+    """A length that the table has no pages for is recorded, once and with the call's site; the
+    sequence attends to the tokens that its table holds, the others are as always."""
+    from long_context_attention_fwd_b200 import capi, ops
+    ps, width, Hkv, D = 16, 2, 2, 64
+    B, P = len(lens), 2 * len(lens)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    table = torch.randperm(P, generator=gen, device="cuda").to(torch.int32).view(B, width).contiguous()
+    kv = [torch.randn(P, ps, Hkv, D, generator=gen, device="cuda").bfloat16() for _ in range(2)]
+    q = torch.randn(B, 4, D, generator=gen, device="cuda").bfloat16()
+    if four:
+        pages = ops.kv4_pages(P, ps, Hkv, D)
+        ops.attn_append_kv4(kv[0].view(-1, Hkv, D), kv[1].view(-1, Hkv, D), pages,
+                            dev(np.arange(P, dtype=np.int32)[:, None]),
+                            torch.full((P,), ps, dtype=torch.int32, device="cuda"),
+                            cu_seqlens=dev(np.arange(0, P * ps + 1, ps, dtype=np.int32)))
+        run = lambda n: ops.attn_decode_kv4(q, pages, table, n)      # noqa: E731
+    else:
+        run = lambda n: ops.attn_decode_paged(q, *kv, table, n)      # noqa: E731
+    lens = np.array(lens, dtype=np.int32)
+    want = run(dev(np.minimum(lens, ps * width)))
+    ok_status()
+    got = run(dev(lens))
+    st, site = status()
+    assert st == capi.ATTN_ERR_INVALID_ARG and site == (0x503 if four else 0x502)
+    ok_status()
+    assert same(got, want)
