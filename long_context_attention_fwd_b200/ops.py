@@ -378,6 +378,8 @@ def _append_args(k, v, block_table, cache_len, q, rope, interleaved, cu_seqlens,
         rope_len, rope_dim = rc.shape[0], 2 * rc.shape[1]
         if rope_dim > D or rope_dim < 16 or rope_dim % 16:
             raise ValueError("the number of rotated elements must be a multiple of 16 up to D")
+        if rope_len < 1:   # no memory: the C entry would take the null address for "no rotation"
+            raise ValueError("rope needs rows of positions")
         cos, sin = rc.data_ptr(), rs.data_ptr()
     if q is not None:
         if rope is None:

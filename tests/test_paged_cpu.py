@@ -173,3 +173,18 @@ def test_sequence_search_finds_the_token_and_stays_inside():
         junk = rng.integers(-2 ** 31, 2 ** 31 - 1, B + 1)
         for t in rng.integers(0, 100, 20):
             search(junk, B, int(t))      # malformed offsets: only the reads are checked
+
+
+@pytest.mark.parametrize("with_q", [False, True])
+def test_a_rotation_table_without_rows_is_refused(with_q):
+    """An empty tensor's address is null, which the C entry reads as "no rotation"."""
+    torch = pytest.importorskip("torch")
+    from long_context_attention_fwd_b200 import ops
+    b16 = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)          # noqa: E731
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)             # noqa: E731
+    rope = (torch.ones(3, 32)[:0], torch.ones(3, 32)[:0])
+    args = lambda r: (b16(2, 2, 64), b16(2, 2, 64), i32(2, 1), i32(2), b16(2, 4, 64) if with_q else None,  # noqa: E731
+                      r, False, None, None, 2, 64, torch.device("cpu"))
+    with pytest.raises(ValueError, match="rows"):
+        ops._append_args(*args(rope))
+    ops._append_args(*args((torch.ones(3, 32), torch.ones(3, 32))))
