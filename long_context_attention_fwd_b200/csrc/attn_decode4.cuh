@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
   // own: a block that ends one and begins the next would be last.  Otherwise every item has W places without tiles behind it on
   // the line, what its start and its join cost (64 sequences of 1-600 tokens: 55 us without
   // them, 19 with them).
-  int chunk = share();
+  int chunk = max(share(), 1);  // 0 without a token in the batch
   const bool apart = p.B <= 32 && (4 * p.B * nv <= grid || (longest <= 2 * W && live <= grid));
   if (apart) {
     const int n = lane < p.B ? tiles_of(length_of(p, lane)) : 0;

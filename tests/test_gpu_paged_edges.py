@@ -46,3 +46,44 @@ def test_decode_records_a_length_past_the_table(four, lens):
     assert st == capi.ATTN_ERR_INVALID_ARG and site == (0x503 if four else 0x502)
     ok_status()
     assert same(got, want)
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("B", [1, 3, 32, 33, 100])
+@pytest.mark.parametrize("length", [0, -5])
+def test_decode_of_empty_sequences_only(four, B, length):
+    """A batch without a token: outputs 0, log-sums minus infinity, nothing else touched; also in a
+    captured step whose sequences grow between replays."""
+    from long_context_attention_fwd_b200 import ops
+    Hq, Hkv, D, ps, n = 8, 2, 128, 16, 5
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    table = torch.arange(B, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    q = torch.randn(B, Hq, D, generator=gen, device="cuda").bfloat16()
+    k, v = (torch.randn(B * n, Hkv, D, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    full = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    cu = torch.arange(0, B * n + 1, n, dtype=torch.int32, device="cuda")
+    if four:
+        pool = (poison((B, Hkv, 1, 18 * D), torch.uint8),)
+    else:
+        pool = (poison((B, ps, Hkv, D), torch.bfloat16), poison((B, ps, Hkv, D), torch.bfloat16))
+    append, decode = (ops.attn_append_kv4, ops.attn_decode_kv4) if four else (ops.attn_append_kv, ops.attn_decode_paged)
+    append(k, v, *pool, table, full, cu_seqlens=cu)
+    want = decode(q, *pool, table, full)
+    lens = torch.full((B,), length, dtype=torch.int32, device="cuda")
+    o, lse = poison((B, Hq, D), torch.bfloat16), poison((B, Hq), torch.float32)
+    decode(q, *pool, table, lens, out=o, lse=lse)
+    assert bool((o == 0).all()) and bool((lse == -math.inf).all())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, capture_error_mode="relaxed"):
+        decode(q, *pool, table, lens, out=o, lse=lse)
+    for m in (length, n, 0):
+        lens.fill_(m)
+        o.fill_(math.nan)
+        g.replay()
+        torch.cuda.synchronize()
+        if m == n:
+            assert same((o, lse), want)
+        else:
+            assert bool((o == 0).all()) and bool((lse == -math.inf).all())
+    ok_status()
+    del g
