@@ -95,7 +95,7 @@ struct Params {
   unsigned long long tag;
   __nv_bfloat16* o;           // [B][Hq][D]
   float* lse;                 // [B][Hq]
-  float scale_log2;
+  float up_scale, scale_log2; // 2^11 scale log2(e) as a product; the second is above 0 (masked scores are -inf)
   unsigned* status;
 };
 
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
     const int nh = min(C::HEADS, p.G - rb * C::HEADS);
 
     uint32_t qf[NG][4][NT][2];
-    float qsum[NG][NT][2], csc[NT][2];
+    float qsum[NG][NT][2], up_h[NT][2];
     float ref[NT][2], l_run[NT][2], om[NG][NT][2];
     float oacc[NG][4][NT][4];
 #pragma unroll
@@ -362,7 +362,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
         float x[NG][2][8], big = 0.f, sum[NG];
 #pragma unroll
         for (int gg = 0; gg < NG; ++gg) {
-          sum[gg] = 0.f;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -374,22 +373,28 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
               x[gg][i][2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              big = fmaxf(big, fabsf(x[gg][i][k]));
-              sum[gg] += x[gg][i][k];
-            }
+            for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(x[gg][i][k]));
           }
         }
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-#pragma unroll
-          for (int gg = 0; gg < NG; ++gg) sum[gg] += __shfl_xor_sync(0xffffffffu, sum[gg], o);
-        }
+        for (int o = 1; o < 4; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
         // down = 2^(13 - ex) brings the row's largest element into [2^13, 2^14); up = 2^ex.
         const int ex = min(max(int((__float_as_uint(big) >> 23) & 0xff) - 127, -114), 127);
         const float down = __uint_as_float(uint32_t(140 - ex) << 23);
         const float up = __uint_as_float(uint32_t(127 + ex) << 23);
+#pragma unroll
+        for (int gg = 0; gg < NG; ++gg) {   // the scaled elements and their sum, which stays in fp32's range
+          sum[gg] = 0.f;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              x[gg][i][k] *= down;
+              sum[gg] += x[gg][i][k];
+            }
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1) sum[gg] += __shfl_xor_sync(0xffffffffu, sum[gg], o);
+        }
 #pragma unroll
         for (int gg = 0; gg < NG; ++gg)
 #pragma unroll
@@ -399,18 +404,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
 #pragma unroll
               for (int k = 0; k < 2; ++k)  // k = 1: upper nibbles, 16 times too large
                 qf[gg][2 * i + h][nt][k] =
-                    pack_f16x2(x[gg][i][2 * h + k] * down * (k ? 0.0625f : 1.f),
-                               x[gg][i][2 * h + k + 4] * down * (k ? 0.0625f : 1.f));
+                    pack_f16x2(x[gg][i][2 * h + k] * (k ? 0.0625f : 1.f),
+                               x[gg][i][2 * h + k + 4] * (k ? 0.0625f : 1.f));
         // To the accumulator's layout: heads 2c and 2c + 1.  An accumulator holds
-        // 2^(13 - ex - 24) times the sum of q code.
+        // 2^(13 - ex - 24) times the sum of q code; 2^ex and the rest (with the exponential's
+        // argument) come back one after the other, since their product can leave fp32 where the
+        // score does not.
 #pragma unroll
         for (int e2 = 0; e2 < 2; ++e2) {
           const int src = 4 * (2 * c + e2);
-          csc[nt][e2] = __shfl_sync(0xffffffffu, up, src) * p.scale_log2 * 2048.f;
-          const float dn = __shfl_sync(0xffffffffu, down, src);
+          up_h[nt][e2] = __shfl_sync(0xffffffffu, up, src) * p.up_scale;
 #pragma unroll
           for (int gg = 0; gg < NG; ++gg)
-            qsum[gg][nt][e2] = __shfl_sync(0xffffffffu, sum[gg], src) * dn * 5.9604644775390625e-8f;
+            qsum[gg][nt][e2] = __shfl_sync(0xffffffffu, sum[gg], src) * 5.9604644775390625e-8f;
         }
       }
     }
@@ -433,7 +439,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
         __syncwarp();
       }
 
-      // scores x, times log2(e)
+      // scores over the rest of their scale, x: x scale_log2 is in units of log2
       float x[TU][NT][4];
 #pragma unroll
       for (int u = 0; u < TU; ++u) {
@@ -485,7 +491,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[u][nt][k] = sc[nt][k] * csc[nt][k & 1];
+          for (int k = 0; k < 4; ++k) x[u][nt][k] = sc[nt][k] * up_h[nt][k & 1];
       }
       if (left < kTile) {
 #pragma unroll
@@ -527,8 +533,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-              const float p0 = ex2_approx(x[u][nt][2 * hh] - ref[nt][0]);
-              const float p1 = ex2_approx(x[u][nt][2 * hh + 1] - ref[nt][1]);
+              const float p0 = ex2_approx(fmaf(x[u][nt][2 * hh], p.scale_log2, -ref[nt][0]));
+              const float p1 = ex2_approx(fmaf(x[u][nt][2 * hh + 1], p.scale_log2, -ref[nt][1]));
               pr[u][nt][2 * hh] = p0;
               pr[u][nt][2 * hh + 1] = p1;
               top_p = fmax3(top_p, p0, p1);
@@ -557,7 +563,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
 #pragma unroll
                 for (int gg = 0; gg < NG; ++gg)
                   s = fmax3(s, step_of(vs[u][hh][gg]), fabsf(low_of(vs[u][hh][gg])) * kMinimumShare);
-                y = fmaxf(y, x[u][nt][2 * hh + e2] + __log2f(s));
+                y = fmaxf(y, fmaf(x[u][nt][2 * hh + e2], p.scale_log2, __log2f(s)));
               }
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));

@@ -911,7 +911,9 @@ attn_status attn_decode_kv4(const void* q, const void* pages, const int32_t* blo
   p.tag = next_decode_tag();
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  const bool huge = std::fabs(scale) > 1e30f;
+  p.up_scale = std::copysign(huge ? 2048.f : 1.f, scale);
+  p.scale_log2 = positive_log2(scale * (huge ? 1.f : 2048.f));
   p.status = dev->status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto launch = [&](auto kernel, auto cfg) {

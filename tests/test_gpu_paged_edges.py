@@ -87,3 +87,25 @@ def test_decode_of_empty_sequences_only(four, B, length):
             assert bool((o == 0).all()) and bool((lse == -math.inf).all())
     ok_status()
     del g
+
+
+@pytest.mark.parametrize("qe,ke,scale,positive", [
+    (119, -116, None, False), (122, -119, None, True), (126, -110, 2.0 ** -14, True), (100, -97, None, True),
+    (-100, 100, None, False)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_4bit_large_queries(qe, ke, scale, positive, D):
+    """Queries up to 2^127 over keys so small that the scores are ordinary; all of one sign, so that
+    their sums leave fp32."""
+    from long_context_attention_fwd_b200 import ops
+    lens, Hq, Hkv, ps = [200, 37], 12, 2, 32
+    rng, q, kv = decode_inputs(lens, Hq, Hkv, D, 63)
+    if positive:
+        q = np.minimum(np.abs(q), 1.9)
+    q = paged.bf16(q * 2.0 ** qe)
+    for k, _ in kv:
+        k[:] = paged.bf16(k * 2.0 ** ke)
+    table, P = paged.table_for(rng, lens, ps)
+    pages, vals = pages4_of(kv, lens, table, P, ps, Hkv, D)
+    o, lse = ops.attn_decode_kv4(to_torch(q), dev(pages), dev(table), dev(np.array(lens, dtype=np.int32)), scale=scale)
+    ok_status()
+    check_decode4(o, lse, q, vals, lens, Hkv, D, 1 / math.sqrt(D) if scale is None else scale)
