@@ -65,11 +65,14 @@ constexpr float kTopMinimum = 1024.f;
 
 constexpr int kMaxParts = 160;                   // blocks that can share a (sequence, kv head)
 
-// NT blocks of 8 heads per pass; a kv head with more than 8 query heads takes passes of 16.
+// NT blocks of 8 heads per pass; a kv head with more than 8 query heads takes passes of 16, whose tiles
+// are computed in halves: the scores and weights of 64 tokens and 16 heads spilled (64 / 4 heads, 48
+// sequences of 1-32K: 155 us, in halves 146).
 template <int D, int NT>
 struct Cfg {
   static constexpr int W = 8;                 // warps
   static constexpr int NS = 2;                // ring stages of a warp
+  static constexpr int TR = kTileUnits / NT;  // units whose scores and weights are in registers at a time
   static constexpr int THREADS = W * 32;
   static constexpr int HEADS = 8 * NT;
   static constexpr int TILE_BYTES = kTileUnits * page::Unit<D>::BYTES;
@@ -166,7 +169,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
   using U = page::Unit<D>;
   constexpr int NG = U::NG;
   constexpr int W = C::W;
-  constexpr int TU = kTileUnits;
+  constexpr int TU = kTileUnits, TR = C::TR;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = lane >> 2, c = lane & 3;
@@ -424,12 +427,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
     for (bool first = true; tw < e; tw += W, first = false, st = st + 1 == C::NS ? 0 : st + 1) {
       asm volatile("cp.async.wait_group %0;" ::"n"(C::NS - 1) : "memory");
       __syncwarp();
-      uint8_t* tile = ring + st * C::TILE_BYTES;
-      const int left = L - (item.j + (tw - t)) * kTile;   // tokens from the tile's first on
-      if (left < kTile) {
+      uint8_t* whole = ring + st * C::TILE_BYTES;
+      const int have = L - (item.j + (tw - t)) * kTile;   // tokens from the tile's first on
+      if (have < kTile) {
         // Behind the length lies anything: codes are harmless, scales are not.
-        for (int i = left + lane; i < kTile; i += 32) {
-          uint8_t* unit = tile + (i >> 4) * U::BYTES;
+        for (int i = have + lane; i < kTile; i += 32) {
+          uint8_t* unit = whole + (i >> 4) * U::BYTES;
 #pragma unroll
           for (int gg = 0; gg < NG; ++gg) {
             reinterpret_cast<uint32_t*>(unit + U::OFF_KS)[(i & 15) * NG + gg] = 0u;
@@ -439,193 +442,199 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
         __syncwarp();
       }
 
-      // scores over the rest of their scale, x: x scale_log2 is in units of log2
-      float x[TU][NT][4];
+#pragma unroll 1
+      for (int part = 0; part < NT; ++part) {
+        const uint8_t* tile = whole + part * TR * U::BYTES;
+        const int left = have - part * TR * page::kUnit;
+        if (NT > 1 && left <= 0) break;
+        // scores over the rest of their scale, x: x scale_log2 is in units of log2
+        float x[TR][NT][4];
 #pragma unroll
-      for (int u = 0; u < TU; ++u) {
-        const uint8_t* unit = tile + u * U::BYTES;
-        uint32_t w[2][2 * NG];   // [token half][NG * word + group]
-        uint32_t sm[2][NG];
+        for (int u = 0; u < TR; ++u) {
+          const uint8_t* unit = tile + u * U::BYTES;
+          uint32_t w[2][2 * NG];   // [token half][NG * word + group]
+          uint32_t sm[2][NG];
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const uint8_t* src = unit + U::OFF_KC + (key0 + 8 * hh) * U::CODE + c * 8 * NG;
-          const uint8_t* ssrc = unit + U::OFF_KS + (key0 + 8 * hh) * U::SCALE;
-          if constexpr (NG == 2) {
-            const uint4 v = *reinterpret_cast<const uint4*>(src);
-            w[hh][0] = v.x, w[hh][1] = v.y, w[hh][2] = v.z, w[hh][3] = v.w;
-            const uint2 y = *reinterpret_cast<const uint2*>(ssrc);
-            sm[hh][0] = y.x, sm[hh][1] = y.y;
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(src);
-            w[hh][0] = v.x, w[hh][1] = v.y;
-            sm[hh][0] = *reinterpret_cast<const uint32_t*>(ssrc);
-          }
-        }
-        float sc[NT][4];
-#pragma unroll
-        for (int gg = 0; gg < NG; ++gg) {
-          float acc[NT][4];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) acc[nt][k] = 0.f;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t x0 = w[0][NG * i + gg], x1 = w[1][NG * i + gg];
-            const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_f16(acc[nt], x0 & kLowNibbles, x1 & kLowNibbles, x0 & kHighNibbles, x1 & kHighNibbles, qf[gg][2 * i][nt]);
-              mma_f16(acc[nt], y0 & kLowNibbles, y1 & kLowNibbles, y0 & kHighNibbles, y1 & kHighNibbles, qf[gg][2 * i + 1][nt]);
+          for (int hh = 0; hh < 2; ++hh) {
+            const uint8_t* src = unit + U::OFF_KC + (key0 + 8 * hh) * U::CODE + c * 8 * NG;
+            const uint8_t* ssrc = unit + U::OFF_KS + (key0 + 8 * hh) * U::SCALE;
+            if constexpr (NG == 2) {
+              const uint4 v = *reinterpret_cast<const uint4*>(src);
+              w[hh][0] = v.x, w[hh][1] = v.y, w[hh][2] = v.z, w[hh][3] = v.w;
+              const uint2 y = *reinterpret_cast<const uint2*>(ssrc);
+              sm[hh][0] = y.x, sm[hh][1] = y.y;
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(src);
+              w[hh][0] = v.x, w[hh][1] = v.y;
+              sm[hh][0] = *reinterpret_cast<const uint32_t*>(ssrc);
             }
           }
+          float sc[NT][4];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int gg = 0; gg < NG; ++gg) {
+            float acc[NT][4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float s = step_of(sm[k >> 1][gg]), m = low_of(sm[k >> 1][gg]);
-              const float y = m * qsum[gg][nt][k & 1];
-              sc[nt][k] = gg == 0 ? fmaf(s, acc[nt][k], y) : sc[nt][k] + fmaf(s, acc[nt][k], y);
-            }
-        }
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+              for (int k = 0; k < 4; ++k) acc[nt][k] = 0.f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[u][nt][k] = sc[nt][k] * up_h[nt][k & 1];
-      }
-      if (left < kTile) {
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t x0 = w[0][NG * i + gg], x1 = w[1][NG * i + gg];
+              const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
 #pragma unroll
-        for (int u = 0; u < TU; ++u)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (u * page::kUnit + key0 + 8 * (k >> 1) >= left) x[u][nt][k] = -INFINITY;
-      }
-
-      // weights p s in fp16; the reference moves when one reaches 2^14 (and on the first tile)
-      uint32_t vs[TU][2][NG];
-#pragma unroll
-      for (int u = 0; u < TU; ++u)
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const uint8_t* ssrc = tile + u * U::BYTES + U::OFF_VS + (key0 + 8 * hh) * U::SCALE;
-          if constexpr (NG == 2) {
-            const uint2 y = *reinterpret_cast<const uint2*>(ssrc);
-            vs[u][hh][0] = y.x, vs[u][hh][1] = y.y;
-          } else {
-            vs[u][hh][0] = *reinterpret_cast<const uint32_t*>(ssrc);
-          }
-        }
-      uint32_t pw[TU][NG][NT][2];
-      float pr[TU][NT][4];
-      float big = 0.f;   // the largest minimum, in magnitude
-#pragma unroll
-      for (int u = 0; u < TU; ++u)
-#pragma unroll
-        for (int gg = 0; gg < NG; ++gg) big = fmax3(big, fabsf(low_of(vs[u][0][gg])), fabsf(low_of(vs[u][1][gg])));
-      auto weigh = [&]() -> bool {
-        uint32_t top = 0u;
-        float top_p = 0.f;
-#pragma unroll
-        for (int u = 0; u < TU; ++u)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const float p0 = ex2_approx(fmaf(x[u][nt][2 * hh], p.scale_log2, -ref[nt][0]));
-              const float p1 = ex2_approx(fmaf(x[u][nt][2 * hh + 1], p.scale_log2, -ref[nt][1]));
-              pr[u][nt][2 * hh] = p0;
-              pr[u][nt][2 * hh + 1] = p1;
-              top_p = fmax3(top_p, p0, p1);
-#pragma unroll
-              for (int gg = 0; gg < NG; ++gg) {
-                const float s = step_of(vs[u][hh][gg]);
-                pw[u][gg][nt][hh] = pack_f16x2(p0 * s, p1 * s);
-                top = max_f16x2(top, pw[u][gg][nt][hh]);
+              for (int nt = 0; nt < NT; ++nt) {
+                mma_f16(acc[nt], x0 & kLowNibbles, x1 & kLowNibbles, x0 & kHighNibbles, x1 & kHighNibbles, qf[gg][2 * i][nt]);
+                mma_f16(acc[nt], y0 & kLowNibbles, y1 & kLowNibbles, y0 & kHighNibbles, y1 & kHighNibbles, qf[gg][2 * i + 1][nt]);
               }
             }
-        return (top & 0xffffu) >= kTopWeight || (top >> 16) >= kTopWeight || top_p >= kTopP || big >= kTopMinimum;
-      };
-      bool move = first;
-      if (!first) move = __any_sync(0xffffffffu, weigh());
-      if (move) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e2 = 0; e2 < 2; ++e2) {
-            float y = -INFINITY;
+              for (int k = 0; k < 4; ++k) {
+                const float s = step_of(sm[k >> 1][gg]), m = low_of(sm[k >> 1][gg]);
+                const float y = m * qsum[gg][nt][k & 1];
+                sc[nt][k] = gg == 0 ? fmaf(s, acc[nt][k], y) : sc[nt][k] + fmaf(s, acc[nt][k], y);
+              }
+          }
 #pragma unroll
-            for (int u = 0; u < TU; ++u)
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[u][nt][k] = sc[nt][k] * up_h[nt][k & 1];
+        }
+        if (left < TR * page::kUnit) {
+#pragma unroll
+          for (int u = 0; u < TR; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (u * page::kUnit + key0 + 8 * (k >> 1) >= left) x[u][nt][k] = -INFINITY;
+        }
+
+        // weights p s in fp16; the reference moves when one reaches 2^14 (and on the first tile)
+        uint32_t vs[TR][2][NG];
+#pragma unroll
+        for (int u = 0; u < TR; ++u)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const uint8_t* ssrc = tile + u * U::BYTES + U::OFF_VS + (key0 + 8 * hh) * U::SCALE;
+            if constexpr (NG == 2) {
+              const uint2 y = *reinterpret_cast<const uint2*>(ssrc);
+              vs[u][hh][0] = y.x, vs[u][hh][1] = y.y;
+            } else {
+              vs[u][hh][0] = *reinterpret_cast<const uint32_t*>(ssrc);
+            }
+          }
+        uint32_t pw[TR][NG][NT][2];
+        float pr[TR][NT][4];
+        float big = 0.f;   // the largest minimum, in magnitude
+#pragma unroll
+        for (int u = 0; u < TR; ++u)
+#pragma unroll
+          for (int gg = 0; gg < NG; ++gg) big = fmax3(big, fabsf(low_of(vs[u][0][gg])), fabsf(low_of(vs[u][1][gg])));
+        auto weigh = [&]() -> bool {
+          uint32_t top = 0u;
+          float top_p = 0.f;
+#pragma unroll
+          for (int u = 0; u < TR; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int hh = 0; hh < 2; ++hh) {
-                float s = kSmallStep;
+                const float p0 = ex2_approx(fmaf(x[u][nt][2 * hh], p.scale_log2, -ref[nt][0]));
+                const float p1 = ex2_approx(fmaf(x[u][nt][2 * hh + 1], p.scale_log2, -ref[nt][1]));
+                pr[u][nt][2 * hh] = p0;
+                pr[u][nt][2 * hh + 1] = p1;
+                top_p = fmax3(top_p, p0, p1);
 #pragma unroll
-                for (int gg = 0; gg < NG; ++gg)
-                  s = fmax3(s, step_of(vs[u][hh][gg]), fabsf(low_of(vs[u][hh][gg])) * kMinimumShare);
-                y = fmaxf(y, fmaf(x[u][nt][2 * hh + e2], p.scale_log2, __log2f(s)));
+                for (int gg = 0; gg < NG; ++gg) {
+                  const float s = step_of(vs[u][hh][gg]);
+                  pw[u][gg][nt][hh] = pack_f16x2(p0 * s, p1 * s);
+                  top = max_f16x2(top, pw[u][gg][nt][hh]);
+                }
               }
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
-            const float was = ref[nt][e2];
-            y = fmaxf(was, y - kFirstWeight);
-            const float alpha = first ? 0.f : ex2_approx(was - y);
-            ref[nt][e2] = y == -INFINITY ? 0.f : y;
-            l_run[nt][e2] *= alpha;
-#pragma unroll
-            for (int gg = 0; gg < NG; ++gg) {
-              om[gg][nt][e2] *= alpha;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                oacc[gg][i][nt][e2] *= alpha;
-                oacc[gg][i][nt][2 + e2] *= alpha;
-              }
-            }
-          }
-        weigh();
-      }
-
-      // sums and the second product
-#pragma unroll
-      for (int u = 0; u < TU; ++u) {
-        const uint8_t* unit = tile + u * U::BYTES;
-        uint32_t wv[4][NG];   // tokens of pair slots 2c, 2c + 1, 2c + 8, 2c + 9
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint8_t* src = unit + U::OFF_VC + (token_of(2 * c + (k & 1)) + 8 * (k >> 1)) * U::CODE + r * 4 * NG;
-          if constexpr (NG == 2) {
-            const uint2 v = *reinterpret_cast<const uint2*>(src);
-            wv[k][0] = v.x, wv[k][1] = v.y;
-          } else {
-            wv[k][0] = *reinterpret_cast<const uint32_t*>(src);
-          }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) l_run[nt][k & 1] += pr[u][nt][k];
-#pragma unroll
-        for (int gg = 0; gg < NG; ++gg) {
-          uint32_t pb[NT][2];
+          return (top & 0xffffu) >= kTopWeight || (top >> 16) >= kTopWeight || top_p >= kTopP || big >= kTopMinimum;
+        };
+        bool move = first && part == 0;
+        if (!move) move = __any_sync(0xffffffffu, weigh());
+        if (move) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const float m = low_of(vs[u][hh][gg]);
-              om[gg][nt][0] = fmaf(pr[u][nt][2 * hh], m, om[gg][nt][0]);
-              om[gg][nt][1] = fmaf(pr[u][nt][2 * hh + 1], m, om[gg][nt][1]);
-              pb[nt][hh] = transpose8x8(pw[u][gg][nt][hh]);
-            }
-          uint32_t a = __byte_perm(wv[0][gg], wv[1][gg], 0x5410), b = __byte_perm(wv[0][gg], wv[1][gg], 0x7632);
-          uint32_t cc = __byte_perm(wv[2][gg], wv[3][gg], 0x5410), d = __byte_perm(wv[2][gg], wv[3][gg], 0x7632);
+            for (int e2 = 0; e2 < 2; ++e2) {
+              float y = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 4; i += 2) {   // rows r: element i of the word; rows r + 8: element i + 4
+              for (int u = 0; u < TR; ++u)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_f16(oacc[gg][i][nt], a & kLowNibbles, b & kLowNibbles, cc & kLowNibbles, d & kLowNibbles, pb[nt]);
-              mma_f16(oacc[gg][i + 1][nt], a & kHighNibbles, b & kHighNibbles, cc & kHighNibbles, d & kHighNibbles, pb[nt]);
+                for (int hh = 0; hh < 2; ++hh) {
+                  float s = kSmallStep;
+#pragma unroll
+                  for (int gg = 0; gg < NG; ++gg)
+                    s = fmax3(s, step_of(vs[u][hh][gg]), fabsf(low_of(vs[u][hh][gg])) * kMinimumShare);
+                  y = fmaxf(y, fmaf(x[u][nt][2 * hh + e2], p.scale_log2, __log2f(s)));
+                }
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+              const float was = ref[nt][e2];
+              y = fmaxf(was, y - kFirstWeight);
+              const float alpha = first && part == 0 ? 0.f : ex2_approx(was - y);
+              ref[nt][e2] = y == -INFINITY ? 0.f : y;
+              l_run[nt][e2] *= alpha;
+#pragma unroll
+              for (int gg = 0; gg < NG; ++gg) {
+                om[gg][nt][e2] *= alpha;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  oacc[gg][i][nt][e2] *= alpha;
+                  oacc[gg][i][nt][2 + e2] *= alpha;
+                }
+              }
             }
-            a >>= 8, b >>= 8, cc >>= 8, d >>= 8;
+          weigh();
+        }
+
+        // sums and the second product
+#pragma unroll
+        for (int u = 0; u < TR; ++u) {
+          const uint8_t* unit = tile + u * U::BYTES;
+          uint32_t wv[4][NG];   // tokens of pair slots 2c, 2c + 1, 2c + 8, 2c + 9
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint8_t* src = unit + U::OFF_VC + (token_of(2 * c + (k & 1)) + 8 * (k >> 1)) * U::CODE + r * 4 * NG;
+            if constexpr (NG == 2) {
+              const uint2 v = *reinterpret_cast<const uint2*>(src);
+              wv[k][0] = v.x, wv[k][1] = v.y;
+            } else {
+              wv[k][0] = *reinterpret_cast<const uint32_t*>(src);
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) l_run[nt][k & 1] += pr[u][nt][k];
+#pragma unroll
+          for (int gg = 0; gg < NG; ++gg) {
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                const float m = low_of(vs[u][hh][gg]);
+                om[gg][nt][0] = fmaf(pr[u][nt][2 * hh], m, om[gg][nt][0]);
+                om[gg][nt][1] = fmaf(pr[u][nt][2 * hh + 1], m, om[gg][nt][1]);
+                pb[nt][hh] = transpose8x8(pw[u][gg][nt][hh]);
+              }
+            uint32_t a = __byte_perm(wv[0][gg], wv[1][gg], 0x5410), b = __byte_perm(wv[0][gg], wv[1][gg], 0x7632);
+            uint32_t cc = __byte_perm(wv[2][gg], wv[3][gg], 0x5410), d = __byte_perm(wv[2][gg], wv[3][gg], 0x7632);
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {   // rows r: element i of the word; rows r + 8: element i + 4
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma_f16(oacc[gg][i][nt], a & kLowNibbles, b & kLowNibbles, cc & kLowNibbles, d & kLowNibbles, pb[nt]);
+                mma_f16(oacc[gg][i + 1][nt], a & kHighNibbles, b & kHighNibbles, cc & kHighNibbles, d & kHighNibbles, pb[nt]);
+              }
+              a >>= 8, b >>= 8, cc >>= 8, d >>= 8;
+            }
           }
         }
       }
