@@ -19,12 +19,16 @@
 //   A nibble needs no conversion: masked out of its word it is the fp16 subnormal code * 2^-24
 //   (or code * 2^-20, the upper nibble of a byte), which the tensor cores multiply exactly; one
 //   AND makes two operands.  The powers of two go into q (K) and into the final scale (V).
-//   K: q is scaled by a power of two to fp16, exact but for 2^-37 of the row's largest element.
+//   K: q is scaled by a power of two to fp16, exact but for 2^-38 of the row's largest element, 2^-34
+//      for the elements that meet upper nibbles.
 //   V: the words of two tokens are interleaved by byte permutes, so that the nibbles of a pair of
 //      tokens land in one register.  The weights p s are rounded to fp16, a relative 2^-11 of
-//      each weight where bf16 would cost 2^-8.  fp16's range is kept by the softmax's reference
-//      R_h, which is not the largest score but moves so that p s, p = 2^(x - R), stays below 2^14
-//      and its largest value so far is at least 1; sums of p and of p m are fp32.
+//      each weight where bf16 would cost 2^-8 (2^-25 below 2^-14).  fp16's range is kept by the
+//      softmax's reference R_h, which is not the largest score but moves so that p s, p = 2^(x - R),
+//      stays below 2^14 and its largest value over both groups so far is at least 1; sums of p and of
+//      p m are fp32.  A group whose steps are so far below the other's that its weights are lost in
+//      this shared range is done again in fp32 (plain_tiles): from ratios of 2^9 on where one of
+//      thousands of tokens has all the weight, of 2^13 or more where many share it.
 //
 // Work: the tiles (kTile tokens of one kv head) of all sequences form one line, with empty places
 // for each start, cut into equal parts, one per block, whatever the lengths.  A block's warps take its tiles in turn; each has
@@ -162,6 +166,110 @@ struct Cursor {
     return passed;
   }
 };
+
+// A warp's tiles of an item (ntile of them, from `tile` on, `every` apart) in plain fp32, where steps
+// of any size keep their part; some ten times slower than the products (48 sequences of 1-32K, 28 / 4
+// heads, all in doubt: 1.0 ms; a group without steps: 35 us to find that out).  few: the groups in
+// doubt; where all their steps are 0, nothing is in doubt and nothing is done.  q: the
+// heads' rows; row: the sequence's pages; out, out_l: normalised outputs [nh][D] and log2 sums [nh].
+template <int D>
+__device__ __forceinline__ void plain_tiles(const Params& p, const __nv_bfloat16* q, const int32_t* row, int g, int nh,
+                                            int tile, int ntile, int every, int L, unsigned few, float* out, float* out_l) {
+  using U = page::Unit<D>;
+  static_assert(U::NG == 2, "a half warp for each group");
+  const int lane = threadIdx.x & 31, upp_log = p.log_ps - 4;
+  auto unit_at = [&](int u) {
+    int pg = __ldg(row + (u >> upp_log));
+    if (pg < 0 || pg >= p.num_pages) pg = 0;            // recorded by the copies
+    return p.pages + ((((long long)pg * p.Hkv + g) << upp_log) + (u & ((1 << upp_log) - 1))) * U::BYTES;
+  };
+  unsigned steps = 0u;                                  // groups with a step above 0
+  for (int i = lane; i < ntile * kTile; i += 32) {
+    const int t = (tile + i / kTile * every) * kTile + i % kTile;
+    if (t >= L) break;
+    const uint2 sm = *reinterpret_cast<const uint2*>(unit_at(t >> 4) + U::OFF_VS + (t & 15) * U::SCALE);
+    steps |= (sm.x & 0xffffu ? 1u : 0u) | (sm.y & 0xffffu ? 2u : 0u);
+  }
+  if (!(__reduce_or_sync(0xffffffffu, steps) & few)) return;
+
+  const float scale_log2 = p.up_scale * 0x1p-11f * p.scale_log2;
+  const int tok = lane & 15, half = lane >> 4;          // scores: a half of a token
+  const int vw = lane >> 1, vj = 4 * (lane & 1);        // outputs: four elements of word vw
+  const int vg = vw % U::NG, vd = 64 * vg + 8 * (vw / U::NG) + vj;
+  constexpr int NH = 4;                                 // heads at a time, the last ones twice
+  for (int h0 = 0; h0 < nh; h0 += NH) {
+    float m[NH], l[NH], o[NH][4];
+#pragma unroll
+    for (int k = 0; k < NH; ++k) m[k] = -INFINITY, l[k] = o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < ntile * kTileUnits; ++i) {
+      const int u = (tile + i / kTileUnits * every) * kTileUnits + i % kTileUnits;
+      const int left = L - u * page::kUnit;
+      if (left <= 0) break;
+      const uint8_t* unit = unit_at(u);
+      const uint32_t* kw = reinterpret_cast<const uint32_t*>(unit + U::OFF_KC + tok * U::CODE) + half;
+      const uint32_t ks = reinterpret_cast<const uint32_t*>(unit + U::OFF_KS + tok * U::SCALE)[half];
+      uint32_t vc[page::kUnit], vs[page::kUnit];
+#pragma unroll
+      for (int t = 0; t < page::kUnit; ++t) {           // behind the length: nothing
+        vc[t] = t < left ? reinterpret_cast<const uint32_t*>(unit + U::OFF_VC + t * U::CODE)[vw] >> (4 * vj) : 0u;
+        vs[t] = t < left ? reinterpret_cast<const uint32_t*>(unit + U::OFF_VS + t * U::SCALE)[vg] : 0u;
+      }
+      float x[NH] = {};
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const uint32_t codes = kw[U::NG * w];
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = fmaf(step_of(ks), float(codes >> (4 * j) & 15u), low_of(ks));
+#pragma unroll
+        for (int k = 0; k < NH; ++k) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(q + min(h0 + k, nh - 1) * D + 64 * half + 8 * w));
+          const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[k] = fmaf(low_of(e[j]), y[2 * j + 1], fmaf(step_of(e[j]), y[2 * j], x[k]));
+        }
+      }
+      float pr[NH];
+#pragma unroll
+      for (int k = 0; k < NH; ++k) {
+        float y = (x[k] + __shfl_xor_sync(0xffffffffu, x[k], 16)) * scale_log2;
+        if (tok >= left) y = -INFINITY;
+        float top = fmaxf(m[k], y);
+#pragma unroll
+        for (int s = 1; s < 16; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+        const float ref = top == -INFINITY ? 0.f : top, alpha = ex2_approx(m[k] - ref);
+        pr[k] = ex2_approx(y - ref);
+        float sum = pr[k];
+#pragma unroll
+        for (int s = 1; s < 16; s <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        m[k] = top;
+        l[k] = fmaf(l[k], alpha, sum);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[k][j] *= alpha;
+      }
+#pragma unroll
+      for (int t = 0; t < page::kUnit; ++t) {
+        float y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = fmaf(step_of(vs[t]), float(vc[t] >> (4 * j) & 15u), low_of(vs[t]));
+#pragma unroll
+        for (int k = 0; k < NH; ++k) {
+          const float pt = __shfl_sync(0xffffffffu, pr[k], t);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[k][j] = fmaf(pt, y[j], o[k][j]);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < NH; ++k) {
+      const int h = min(h0 + k, nh - 1);
+      const float inv = l[k] == 0.f ? 0.f : 1.f / l[k];
+      *reinterpret_cast<float4*>(out + h * D + vd) = make_float4(o[k][0] * inv, o[k][1] * inv, o[k][2] * inv, o[k][3] * inv);
+      if (lane == 0) out_l[h] = l[k] == 0.f ? -INFINITY : m[k] + log2f(l[k]);
+    }
+  }
+}
 
 template <int D, int NT>
 __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(const Params p) {
@@ -642,6 +750,40 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
       issue(st);
     }
 
+    // ---- groups in doubt.  The groups share a reference, and a group whose steps are far below the
+    // other's has its weights among fp16's subnormals, each wrong by up to 2^-25.  A group is in
+    // doubt where, for any head, the sum of p s code over its 64 elements is so small that this could
+    // make up 2^-10 of their mean, codes being 15 at most.
+    unsigned few = 0u;
+    if constexpr (NG > 1) {
+      const float least = float((tw - t) / W * kTile) * (15.f * 64.f * 0x1p-15f * 0x1p-24f);
+      float sum[NG][NT][2], low = INFINITY;
+#pragma unroll
+      for (int gg = 0; gg < NG; ++gg)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e2 = 0; e2 < 2; ++e2) {   // this lane's eight elements
+            auto two = [&](int i) { return oacc[gg][i][nt][e2] + oacc[gg][i][nt][2 + e2]; };
+            sum[gg][nt][e2] = two(0) + two(2) + 0.0625f * (two(1) + two(3));
+            low = fminf(low, sum[gg][nt][e2]);
+          }
+      if (!__all_sync(0xffffffffu, low >= least)) {
+#pragma unroll
+        for (int gg = 0; gg < NG; ++gg)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e2 = 0; e2 < 2; ++e2) {
+              float y = sum[gg][nt][e2];
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+              if (nt * 8 + 2 * c + e2 < nh && !(y >= least)) few |= 1u << gg;
+            }
+        few = __reduce_or_sync(0xffffffffu, few);
+      }
+    }
+
     // ---- join the warps' parts of this item: normalised outputs, log2 sums
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -670,6 +812,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
           }
         }
       }
+    if constexpr (NG > 1) {
+      if (__builtin_expect(few != 0u, 0)) {   // behind the tile loop in the code: 2% of the call
+        __syncwarp();
+        plain_tiles<D>(p, p.q + ((long long)item.b * p.Hq + h0) * D, p.table + (long long)item.b * p.width, g, nh,
+                       item.j + (tw - t) % W, (tw - t) / W, W, L, few, s_o + warp * C::HEADS * D, s_l + warp * C::HEADS);
+      }
+    }
     __syncthreads();
     const int a_line = t - item.j, e_line = a_line + item.nt;   // the whole item on the line
     const bool shared_item = a_line < t0 || e_line > t1;

@@ -109,3 +109,83 @@ def test_decode_4bit_large_queries(qe, ke, scale, positive, D):
     o, lse = ops.attn_decode_kv4(to_torch(q), dev(pages), dev(table), dev(np.array(lens, dtype=np.int32)), scale=scale)
     ok_status()
     check_decode4(o, lse, q, vals, lens, Hkv, D, 1 / math.sqrt(D) if scale is None else scale)
+
+
+@pytest.mark.parametrize("heads", [(7, 1), (20, 1)], ids=["7", "20"])
+@pytest.mark.parametrize("e0,e1,by_token", [(0, -22, False), (0, 24, False), (-15, 15, False), (20, -20, False),
+                                            (-40, 40, False), (0, -30, True), (15, -15, True), (30, -30, True)])
+def test_decode_4bit_groups_of_very_different_steps(heads, e0, e1, by_token):
+    """The two groups of 64 elements of V differ in size by 2^22 to 2^80, all over or, by token, in
+    turn: each group's outputs are held to its own size, with scores that rise and fall along the
+    sequence and differ from head to head."""
+    from long_context_attention_fwd_b200 import ops
+    (Hq, Hkv), D, ps, lens = heads, 128, 32, [900, 64, 3]
+    rng, q, kv = decode_inputs(lens, Hq, Hkv, D, 61)
+    for b, L in enumerate(lens):
+        k, v = kv[b]
+        k[:] = paged.bf16(k * (1 + 15 * np.abs(np.sin(np.arange(L) / 90))[:, None, None]))
+        size = np.empty((L, 1, D))
+        size[:, :, :64], size[:, :, 64:] = 2.0 ** e0, 2.0 ** e1
+        if by_token:
+            size[1::3] = size[1::3, :, ::-1]
+        v[:] = paged.bf16(v * size)
+    table, P = paged.table_for(rng, lens, ps)
+    pages, vals = pages4_of(kv, lens, table, P, ps, Hkv, D)
+    o, lse = ops.attn_decode_kv4(to_torch(q), dev(pages), dev(table), dev(np.array(lens, dtype=np.int32)))
+    ok_status()
+    check_decode4(o, lse, q, vals, lens, Hkv, D, 1 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("heads", [(7, 1), (20, 1)], ids=["7", "20"])
+@pytest.mark.parametrize("e0,e1", [(0, -5), (6, 0), (0, -8), (-10, 0), (0, -16), (60, -50), (-70, 40)])
+def test_decode_4bit_groups_of_different_steps_all_along(heads, e0, e1):
+    """From alike to far apart, with few and many tokens of the same weight and one of all."""
+    from long_context_attention_fwd_b200 import ops
+    (Hq, Hkv), D, ps, lens = heads, 128, 64, [1500, 130, 65]
+    rng, q, kv = decode_inputs(lens, Hq, Hkv, D, 62)
+    for b, mult in enumerate((1, 0, 40)):
+        k, v = kv[b]
+        k[:] = paged.bf16(k * mult)
+        v[..., :64], v[..., 64:] = paged.bf16(v[..., :64] * 2.0 ** e0), paged.bf16(v[..., 64:] * 2.0 ** e1)
+    table, P = paged.table_for(rng, lens, ps)
+    pages, vals = pages4_of(kv, lens, table, P, ps, Hkv, D)
+    o, lse = ops.attn_decode_kv4(to_torch(q), dev(pages), dev(table), dev(np.array(lens, dtype=np.int32)))
+    ok_status()
+    check_decode4(o, lse, q, vals, lens, Hkv, D, 1 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("heads", [(7, 1), (12, 1)], ids=["7", "12"])
+@pytest.mark.parametrize("first", [0, 1])
+@pytest.mark.parametrize("kind", ["small", "zero", "equal"])
+def test_decode_4bit_one_token_takes_a_head(heads, first, kind):
+    """One head sees one token only, whose steps in one group are 2^-30 of the others' or 0 (elements
+    all zero or all equal), while the other heads see all tokens; then the token is the last one."""
+    from long_context_attention_fwd_b200 import ops
+    (Hq, Hkv), D, ps, lens = heads, 128, 16, [400, 400]
+    rng, q, kv = decode_inputs(lens, Hq, Hkv, D, 64)
+    group = slice(64 * first, 64 * first + 64)
+    for b, at in enumerate((5, 399)):
+        k, v = kv[b]
+        k[at, 0] = paged.bf16(q[b, 0] * 6)
+        x = v[at, 0, group]
+        v[at, 0, group] = {"small": paged.bf16(x * 2.0 ** -30), "zero": 0 * x, "equal": 0 * x + 0.75}[kind]
+    table, P = paged.table_for(rng, lens, ps)
+    pages, vals = pages4_of(kv, lens, table, P, ps, Hkv, D)
+    o, lse = ops.attn_decode_kv4(to_torch(q), dev(pages), dev(table), dev(np.array(lens, dtype=np.int32)))
+    ok_status()
+    check_decode4(o, lse, q, vals, lens, Hkv, D, 1 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("first", [0, 1])
+def test_decode_4bit_a_group_without_steps(first):
+    """A group of V that is constant in every token: its outputs are the weighted minima."""
+    from long_context_attention_fwd_b200 import ops
+    Hq, Hkv, D, ps, lens = 8, 2, 128, 32, [700, 31]
+    rng, q, kv = decode_inputs(lens, Hq, Hkv, D, 65)
+    for _, v in kv:
+        v[..., 64 * first:64 * first + 64] = paged.bf16(rng.normal(size=v.shape[:2] + (1,)))
+    table, P = paged.table_for(rng, lens, ps)
+    pages, vals = pages4_of(kv, lens, table, P, ps, Hkv, D)
+    o, lse = ops.attn_decode_kv4(to_torch(q), dev(pages), dev(table), dev(np.array(lens, dtype=np.int32)))
+    ok_status()
+    check_decode4(o, lse, q, vals, lens, Hkv, D, 1 / math.sqrt(D))
