@@ -189,3 +189,30 @@ def test_decode_4bit_a_group_without_steps(first):
     o, lse = ops.attn_decode_kv4(to_torch(q), dev(pages), dev(table), dev(np.array(lens, dtype=np.int32)))
     ok_status()
     check_decode4(o, lse, q, vals, lens, Hkv, D, 1 / math.sqrt(D))
+
+
+def test_decode_4bit_step_by_step_against_64_bits():
+    """Tokens appended one by one with the rotation, after prompts of two lengths: every decode is
+    the softmax in 64 bits over the values that the pages then hold, key by key and to fp16's
+    rounding of the weights."""
+    from long_context_attention_fwd_b200 import ops
+    lens, Hq, Hkv, D, ps, steps = [70, 33, 0], 8, 2, 128, 32, 4
+    B, total = len(lens), [n + steps for n in lens]
+    rng = np.random.default_rng(71)
+    table, P = paged.table_for(rng, total, ps)
+    rope = tuple(dev(t) for t in rope_table(128, D // 2, 72))
+    pages = poison((P, Hkv, ps // 16, 18 * D), torch.uint8)
+    done = np.zeros(B, dtype=np.int32)
+    for new in [lens] + [[1] * B] * steps:
+        x = to_torch(paged.bf16(2 * rng.normal(size=(sum(new), Hq + 2 * Hkv, D))))
+        done = done + np.array(new, dtype=np.int32)
+        cu = dev(np.concatenate([[0], np.cumsum(new)]).astype(np.int32))
+        q = ops.attn_append_kv4(x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], pages, dev(table), dev(done), q=x[:, :Hq],
+                                rope=rope, cu_seqlens=cu)
+        if new != [1] * B:
+            continue
+        o, lse = ops.attn_decode_kv4(q, pages, dev(table), dev(done))
+        ok_status()
+        qf = f64(bits_of(q)).reshape(B, Hq, D)
+        check_decode4(o, lse, qf, values_of(table, pages.cpu().numpy(), ps, done.tolist(), D), done.tolist(), Hkv, D,
+                      1 / math.sqrt(D))
