@@ -207,7 +207,8 @@ attn_status attn_decode(const void* q, const void* k_cache, const void* v_cache,
  * q may be NULL (with q_out NULL); q_out [T][Hq][D] is contiguous and may be a contiguous q.
  * k goes to k_pages and v to v_pages (attn_append_kv) or, as 4 bits, to pages:
  *     m = min x,  s = bf16((max x - m) / 15),  code = clamp(rint((x - m) / s), 0, 15)
- * over each group of 64 of the bf16 values that bf16 pages would hold (s = 0: codes 0).  A
+ * over each group of 64 of the bf16 values that bf16 pages would hold (s = 0: codes 0).  The
+ * differences and the fifteenth are rounded to fp32; the quotient is not rounded before rint.  A
  * group with a NaN or an infinity, or whose range is not finite in fp32, is stored as s = m =
  * NaN.
  *   - Tokens behind cu_seqlens[B] and tokens at negative positions are left out silently,

@@ -6,8 +6,9 @@
 // with (a, b) = (x[j], x[j + half]) or, interleaved, (x[2j], x[2j + 1]), and writes k and v where
 // the page table says: as bf16, or as 4-bit codes with a step and a minimum per 64 elements,
 //     m = min x,  s = bf16((max x - m) / 15),  code = rint((x - m) / s) in 0..15,
-// of the bf16 values x.  The quotient is rounded as in exact arithmetic: a product with 1 / s
-// gives a candidate, and the remainder x - m - code s, which fp32 holds exactly, corrects it.
+// of the bf16 values x.  The quotient of the fp32 difference a = x - m is rounded as in exact
+// arithmetic: a product with 1 / s gives a candidate, and the remainder a - code s, which fp32 holds
+// exactly, corrects it.
 // (IEEE divisions, 16 a thread, took the 4-bit append three times as long as the bf16 one.)
 // A group with a NaN or an infinity, or whose range leaves fp32, gets s = m = NaN and reads back
 // as NaN.

@@ -441,7 +441,8 @@ def attn_append_kv4(k: torch.Tensor, v: torch.Tensor, pages: torch.Tensor,
                     q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
     """attn_append_kv into 4-bit pages (kv4_pages).  The bf16 values x that bf16 pages would hold
     are kept per group of 64 elements as a minimum m, a step s = bf16((max - m) / 15) and codes
-    clamp(round((x - m) / s), 0, 15); a group with a NaN or an infinity reads back as NaN."""
+    clamp(round((x - m) / s), 0, 15), with the differences in fp32; a group with a NaN or an
+    infinity reads back as NaN."""
     P, Hkv, ps, D = _check_kv4(pages)
     dev = pages.device
     before, sizes, width, q_out = _append_args(k, v, block_table, cache_len, q, rope, interleaved,

@@ -216,3 +216,29 @@ def test_decode_4bit_step_by_step_against_64_bits():
         qf = f64(bits_of(q)).reshape(B, Hq, D)
         check_decode4(o, lse, qf, values_of(table, pages.cpu().numpy(), ps, done.tolist(), D), done.tolist(), Hkv, D,
                       1 / math.sqrt(D))
+
+
+def test_append_4bit_differences_are_rounded_to_fp32():
+    """Elements next to the middle between two codes by less than fp32 keeps of x - m: the code is
+    that of the rounded difference, ties to even."""
+    from long_context_attention_fwd_b200 import ops
+    x = np.zeros((6, 1, 64))
+    tiny = 2.0 ** -30
+    for t, lo in enumerate([-7.5, -8.5, -0.5, -14.5, tiny, -tiny]):    # steps of 1
+        x[t, 0, :5] = lo, (lo + 15 if t < 4 else 15), tiny, -tiny if t != 4 else tiny, 0.0 if t != 4 else tiny
+        x[t, 0, 5:] = 7.5 if t >= 4 else lo
+        x[t, 0, 6:] = 6.5 if t >= 4 else lo
+    assert np.array_equal(paged.bf16(x), x)
+    pages = poison((1, 1, 1, 18 * 64), torch.uint8)
+    k = to_torch(x)
+    cl, cu = dev(np.array([6], dtype=np.int32)), dev(np.array([0, 6], dtype=np.int32))
+    ops.attn_append_kv4(k, k, pages, dev(np.zeros((1, 1), dtype=np.int32)), cl, cu_seqlens=cu)
+    ok_status()
+    got = paged.load4(pages.cpu().numpy(), [0], 16, 6, 64)
+    x32 = x.astype(np.float32)
+    lo = x32.min(-1, keepdims=True)
+    step = ((x32.max(-1, keepdims=True) - lo) / np.float32(15)).astype(np.float64)
+    assert (paged.bf16(step) == 1).all()
+    want = np.rint((x32 - lo).astype(np.float64)).astype(np.uint8)
+    for w in "kv":
+        assert np.array_equal(got[w][0], want) and (got[w][1] == 1).all()
