@@ -17,10 +17,11 @@
 // hold a row in two 16-byte chunks, chosen so that rotation partners meet in one thread, and a
 // thread's angles serve every head of the token.  A warp takes a token, or a share of its rows
 // where there are fewer tokens than warps to fill the SMs; it has kAhead rows' loads in flight,
-// and the first of them do not wait for the page table.  (A block per token: 152 us for 30K
-// tokens of 28 + 2 x 4 heads where a warp per token takes 99, 94% of the copy
-// rate.)  The 4-bit form is bound by issue beside HBM: the codes (16 prompt chunks of up to 4K
-// tokens and their read-back: 174 us, 74%).
+// and the first of them do not wait for the page table.  (A block per token: 152 us for 32K
+// tokens of 28 + 2 x 4 heads where a warp per token takes 98, 94% of the copy
+// rate.)  The 4-bit form waits for its loads (4.6 TB/s) and for issue (68%), neither of them full: a
+// pass's codes follow its own loads (16 prompt chunks of up to 4K tokens and their read-back: 173 us,
+// 75%).
 #pragma once
 #include <cuda_bf16.h>
 
@@ -284,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const Params p) {
 // rows where tokens are few; eight threads
 // hold a row, each the word (or the two words of both groups) of eight elements, so that reads
 // and writes are whole sectors.  Bound by HBM, by the bf16 rows it writes: four bytes of five
-// (8 x 16-32K tokens, 4 heads: 487 MB in 93 us; a plain fill writes 3.9 TB/s).  With one row a lane
+// (8 x 16-32K tokens, 4 heads: 487 MB in 92 us; a plain fill writes 3.9 TB/s).  With one row a lane
 // in flight 32 registers let all 64 warps of an SM in; three rows and 40 took 101 us.
 struct GatherParams {
   page::PageMap map;
@@ -296,7 +297,8 @@ struct GatherParams {
 };
 
 // The eight elements of a word.  A code under the exponent of 2^(23 - 4 j) is 2^(23 - 4 j) + code,
-// which needs neither a shift nor a conversion for the first five.
+// which needs neither a shift nor a conversion for the first five (the case above 92.3 -> 91.4 us,
+// short ones as they were).
 __device__ __forceinline__ uint4 decode_word(uint32_t w, uint32_t sm) {
   const float s = __uint_as_float(sm << 16), m = __uint_as_float(sm & 0xffff0000u);
   const uint32_t w2 = w >> 20;

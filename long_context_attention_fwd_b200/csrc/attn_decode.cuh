@@ -30,8 +30,9 @@
 // to 128 rows each; everything after the loads is the same.  Warp 8 loads K and warp 10 V; their
 // lanes look up the next tile's pages while the current tile's loads wait for room, and each
 // issues its own page's loads (small boxes are bound by their issue: pages of 16 took 287 us for
-// 16 sequences of 16-32K keys with one issuing lane, 197 with eight, 160 with two warps
-// of eight).  A page of the table that is not in the pool is recorded and loads zeros.  The
+// 16 sequences of 16-32K keys with one issuing lane, 197 with eight, 156 with two warps
+// of eight, and 168 once a run of calls has the power cap lower the SM clock from 1965 to 1720 MHz).
+// A page of the table that is not in the pool is recorded and loads zeros.  The
 // partial results are fp32 (the dense form's are bf16, one more rounding of 2^-8 each); the
 // weights are bf16 for the product with V, summed as rounded, as in the forward kernel.
 //

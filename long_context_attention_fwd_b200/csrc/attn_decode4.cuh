@@ -39,10 +39,12 @@
 // the pair is shared with other blocks, each writes its part and the last one to finish joins
 // them (done flags with the call's tag, as attn_decode_kernel does).
 //
-// Measured, D = 128, 28 / 4 heads: 48 sequences of 1-32K tokens in pages of 16, 389 MB, 98 us
-// (4.0 TB/s, 61% of the copy rate); one of 32K, 15 us; one of 513, 9 us.  The first is bound by
-// issue (when it took 102 us: without the copies 81, without the products 72, without both 44; an
-// m16n8k16 holds its scheduler's issue for about 7 of its 8 cycles).  The others are latency: the length,
+// Measured, D = 128, 28 / 4 heads: 48 sequences of 1-32K tokens in pages of 16, 391 MB, 96 us
+// (4.1 TB/s, 62% of the copy rate); one of 32K, 14.4 us; one of 513, 9 us.  64 / 4 heads: 147 and
+// (16 / 1) 20.8 us.  The first fills no pipe (issue and ALU are active half of the time, tensor a
+// quarter): with two warps a scheduler, the copies, the conversions and the products largely add up
+// (when it took 102 us: without the copies 81, without the products 72, without both 44; an m16n8k16
+// holds its scheduler's issue for about 7 of its 8 cycles).  The others are latency: the length,
 // the page, the codes and the join are loads behind one another.  Eight warps with 64-token tiles
 // are the best of those tried: more warps need smaller tiles, whose scores, weights and copies
 // overlap less (16 warps of 32 tokens 116 us, two blocks of 8 101 us but 20 us for one of 32K).
@@ -307,7 +309,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
     return longest <= 2 * W ? max(x, longest) : x;
   };
   // With few sequences and heads, or short ones and a block for each, each begins at a block of its
-  // own: a block that ends one and begins the next would be last.  Otherwise every item has W places without tiles behind it on
+  // own: a block that ends one and begins the next would be last (28 / 4 heads, 1-600 tokens: 32
+  // sequences 9.0 us so; 33, which a lane each cannot hold, 15.7).  Otherwise every item has W places without tiles behind it on
   // the line, what its start and its join cost (64 sequences of 1-600 tokens: 55 us without
   // them, 19 with them).
   int chunk = max(share(), 1);  // 0 without a token in the batch

@@ -242,3 +242,29 @@ def test_append_4bit_differences_are_rounded_to_fp32():
     want = np.rint((x32 - lo).astype(np.float64)).astype(np.uint8)
     for w in "kv":
         assert np.array_equal(got[w][0], want) and (got[w][1] == 1).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_attention_over_what_the_4bit_cache_keeps(D):
+    """Whole prompts: appended, read back and attended to as one packed batch, rotated q and all."""
+    import oracle
+    from helpers import TOL_LSE, o_error_report
+    from long_context_attention_fwd_b200 import ops
+    lens, Hq, Hkv, ps = [70, 1, 33, 130], 8, 2, 16
+    rng = np.random.default_rng(81)
+    table, P = paged.table_for(rng, lens, ps)
+    cu_h = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    T, cu, cl, tb = int(cu_h[-1]), dev(cu_h), dev(np.array(lens, dtype=np.int32)), dev(table)
+    x = to_torch(paged.bf16(0.5 * rng.normal(size=(T, Hq + 2 * Hkv, D))))
+    pages = poison((P, Hkv, ps // 16, 18 * D), torch.uint8)
+    rope = tuple(dev(t) for t in rope_table(128 + 16, D // 2, 82))
+    q = ops.attn_append_kv4(x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], pages, tb, cl, q=x[:, :Hq], rope=rope, cu_seqlens=cu)
+    k, v = ops.attn_gather_kv4(pages, tb, cl, cu, T)
+    o, lse = ops.attn_fwd(q, k, v, causal=True, cu_seqlens=cu)
+    ok_status()
+    qf, kf, vf = (f64(bits_of(t)).reshape(t.shape) for t in (q, k, v))
+    o_r, l_r = oracle.fwd(qf, kf, vf, True, 1 / math.sqrt(D), cu_seqlens=cu_h)
+    oa_r, _ = oracle.fwd(qf, kf, np.abs(vf), True, 1 / math.sqrt(D), cu_seqlens=cu_h)
+    rep = o_error_report(f64(bits_of(o)).reshape(o.shape), o_r, oa_r, nkeys=max(lens))
+    assert rep["n_over_model"] == 0, rep
+    assert np.abs(lse.double().cpu().numpy() - l_r).max() <= TOL_LSE
