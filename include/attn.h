@@ -254,8 +254,8 @@ attn_status attn_decode_paged(const void* q, const void* k_pages, const void* v_
 /* attn_decode over 4-bit pages: the attention over the values the pages stand for.  Codes enter
  * the products as exact integers and scores are summed in fp32; the weights, times V's
  * steps, are rounded to fp16 for the product with V's codes and summed unrounded (a group of 64
- * elements whose weights fp16 would lose next to the other group's is computed in fp32, some ten
- * times slower).  A table for 2^30 tiles of 64 tokens, a kv head and 16 query heads of it, or more,
+ * elements whose weights fp16 would lose next to the other group's is computed in fp32, some
+ * fifteen times slower).  A table for 2^30 tiles of 64 tokens, a kv head and 16 query heads of it, or more,
  * is refused (eight are counted for the start of each).  Otherwise as attn_decode_paged (workspace
  * rules included). */
 size_t attn_decode_kv4_workspace_size(int B, int Hq, int Hkv, int D, int max_pages, int page_size);

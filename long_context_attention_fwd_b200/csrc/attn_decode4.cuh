@@ -27,7 +27,7 @@
 //      softmax's reference R_h, which is not the largest score but moves so that p s, p = 2^(x - R),
 //      stays below 2^14 and its largest value over both groups so far is at least 1; sums of p and of
 //      p m are fp32.  A group whose steps are so far below the other's that its weights are lost in
-//      this shared range is done again in fp32 (plain_tiles): from ratios of 2^9 on where one of
+//      this shared range is done again in fp32 (plain_tiles): from ratios of about 2^9 on where one of
 //      thousands of tokens has all the weight, of 2^13 or more where many share it.
 //
 // Work: the tiles (kTile tokens of one kv head) of all sequences form one line, with empty places
@@ -39,8 +39,8 @@
 // the pair is shared with other blocks, each writes its part and the last one to finish joins
 // them (done flags with the call's tag, as attn_decode_kernel does).
 //
-// Measured, D = 128, 28 / 4 heads: 48 sequences of 1-32K tokens in pages of 16, 391 MB, 96 us
-// (4.1 TB/s, 62% of the copy rate); one of 32K, 14.4 us; one of 513, 9 us.  64 / 4 heads: 147 and
+// Measured, D = 128, 28 / 4 heads: 48 sequences of 1-32K tokens in pages of 16, 391 MB, 97 us
+// (4.0 TB/s, 62% of the copy rate); one of 32K, 14.4 us; one of 513, 9 us.  64 / 4 heads: 147 and
 // (16 / 1) 20.8 us.  The first fills no pipe (issue and ALU are active half of the time, tensor a
 // quarter): with two warps a scheduler, the copies, the conversions and the products largely add up
 // (when it took 102 us: without the copies 81, without the products 72, without both 44; an m16n8k16
@@ -69,16 +69,17 @@ constexpr float kSmallStep = 3.2311742677852644e-27f;
 constexpr float kTopP = 1.2676506002282294e30f;
 constexpr float kTopMinimum = 1024.f;
 
+constexpr int kEvenSteps = 6;                     // log2: steps this far apart share a reference well
 constexpr int kMaxParts = 160;                   // blocks that can share a (sequence, kv head)
 
 // NT blocks of 8 heads per pass; a kv head with more than 8 query heads takes passes of 16, whose tiles
-// are computed in halves: the scores and weights of 64 tokens and 16 heads spilled (64 / 4 heads, 48
-// sequences of 1-32K: 155 us, in halves 146).
+// are computed in halves at D = 128: the scores and weights of 64 tokens and 16 heads spilled (64 / 4
+// heads, 48 sequences of 1-32K: 155 us, in halves 146; D = 64 does not spill: 114, in halves 120).
 template <int D, int NT>
 struct Cfg {
   static constexpr int W = 8;                 // warps
   static constexpr int NS = 2;                // ring stages of a warp
-  static constexpr int TR = kTileUnits / NT;  // units whose scores and weights are in registers at a time
+  static constexpr int TR = D == 128 ? kTileUnits / NT : kTileUnits;  // units with scores and weights in registers at a time
   static constexpr int THREADS = W * 32;
   static constexpr int HEADS = 8 * NT;
   static constexpr int TILE_BYTES = kTileUnits * page::Unit<D>::BYTES;
@@ -170,10 +171,11 @@ struct Cursor {
 };
 
 // A warp's tiles of an item (ntile of them, from `tile` on, `every` apart) in plain fp32, where steps
-// of any size keep their part; some ten times slower than the products (48 sequences of 1-32K, 28 / 4
-// heads, all in doubt: 1.0 ms; a group without steps: 35 us to find that out).  few: the groups in
-// doubt; where all their steps are 0, nothing is in doubt and nothing is done.  q: the
-// heads' rows; row: the sequence's pages; out, out_l: normalised outputs [nh][D] and log2 sums [nh].
+// of any size keep their part; some fifteen times slower than the products (48 sequences of 1-32K, 28
+// / 4 heads, all done again: 1.6 ms; four heads at a time 1.0, but 1% of every other call).  few: the groups in doubt.  Where all their steps are 0, or no token's
+// two steps are more than about 2^kEvenSteps apart, there is no doubt and nothing is done (35 us in
+// that case).  q: the heads' rows; row: the sequence's pages; out, out_l: normalised outputs [nh][D]
+// and log2 sums [nh].
 template <int D>
 __device__ __forceinline__ void plain_tiles(const Params& p, const __nv_bfloat16* q, const int32_t* row, int g, int nh,
                                             int tile, int ntile, int every, int L, unsigned few, float* out, float* out_l) {
@@ -185,20 +187,22 @@ __device__ __forceinline__ void plain_tiles(const Params& p, const __nv_bfloat16
     if (pg < 0 || pg >= p.num_pages) pg = 0;            // recorded by the copies
     return p.pages + ((((long long)pg * p.Hkv + g) << upp_log) + (u & ((1 << upp_log) - 1))) * U::BYTES;
   };
-  unsigned steps = 0u;                                  // groups with a step above 0
+  unsigned seen = 0u;                                   // groups with a step above 0; steps far apart
   for (int i = lane; i < ntile * kTile; i += 32) {
     const int t = (tile + i / kTile * every) * kTile + i % kTile;
     if (t >= L) break;
     const uint2 sm = *reinterpret_cast<const uint2*>(unit_at(t >> 4) + U::OFF_VS + (t & 15) * U::SCALE);
-    steps |= (sm.x & 0xffffu ? 1u : 0u) | (sm.y & 0xffffu ? 2u : 0u);
+    const int s0 = sm.x & 0xffffu, s1 = sm.y & 0xffffu;
+    seen |= (s0 ? 1u : 0u) | (s1 ? 2u : 0u) | (abs(s0 - s1) > kEvenSteps << 7 ? 4u : 0u);
   }
-  if (!(__reduce_or_sync(0xffffffffu, steps) & few)) return;
+  seen = __reduce_or_sync(0xffffffffu, seen);
+  if (!(seen & few) || !(seen & 4u)) return;
 
   const float scale_log2 = p.up_scale * 0x1p-11f * p.scale_log2;
   const int tok = lane & 15, half = lane >> 4;          // scores: a half of a token
   const int vw = lane >> 1, vj = 4 * (lane & 1);        // outputs: four elements of word vw
   const int vg = vw % U::NG, vd = 64 * vg + 8 * (vw / U::NG) + vj;
-  constexpr int NH = 4;                                 // heads at a time, the last ones twice
+  constexpr int NH = 2;                                 // heads at a time, the last ones twice
   for (int h0 = 0; h0 < nh; h0 += NH) {
     float m[NH], l[NH], o[NH][4];
 #pragma unroll
@@ -476,6 +480,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
         float x[NG][2][8], big = 0.f, sum[NG];
 #pragma unroll
         for (int gg = 0; gg < NG; ++gg) {
+          sum[gg] = 0.f;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -487,28 +492,22 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
               x[gg][i][2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(x[gg][i][k]));
+            for (int k = 0; k < 8; ++k) {
+              big = fmaxf(big, fabsf(x[gg][i][k]));
+              sum[gg] = fmaf(x[gg][i][k], 0x1p-7f, sum[gg]);   // 64 of any size stay in fp32
+            }
           }
         }
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+        for (int o = 1; o < 4; o <<= 1) {
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+#pragma unroll
+          for (int gg = 0; gg < NG; ++gg) sum[gg] += __shfl_xor_sync(0xffffffffu, sum[gg], o);
+        }
         // down = 2^(13 - ex) brings the row's largest element into [2^13, 2^14); up = 2^ex.
         const int ex = min(max(int((__float_as_uint(big) >> 23) & 0xff) - 127, -114), 127);
         const float down = __uint_as_float(uint32_t(140 - ex) << 23);
         const float up = __uint_as_float(uint32_t(127 + ex) << 23);
-#pragma unroll
-        for (int gg = 0; gg < NG; ++gg) {   // the scaled elements and their sum, which stays in fp32's range
-          sum[gg] = 0.f;
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              x[gg][i][k] *= down;
-              sum[gg] += x[gg][i][k];
-            }
-#pragma unroll
-          for (int o = 1; o < 4; o <<= 1) sum[gg] += __shfl_xor_sync(0xffffffffu, sum[gg], o);
-        }
 #pragma unroll
         for (int gg = 0; gg < NG; ++gg)
 #pragma unroll
@@ -518,8 +517,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
 #pragma unroll
               for (int k = 0; k < 2; ++k)  // k = 1: upper nibbles, 16 times too large
                 qf[gg][2 * i + h][nt][k] =
-                    pack_f16x2(x[gg][i][2 * h + k] * (k ? 0.0625f : 1.f),
-                               x[gg][i][2 * h + k + 4] * (k ? 0.0625f : 1.f));
+                    pack_f16x2(x[gg][i][2 * h + k] * down * (k ? 0.0625f : 1.f),
+                               x[gg][i][2 * h + k + 4] * down * (k ? 0.0625f : 1.f));
         // To the accumulator's layout: heads 2c and 2c + 1.  An accumulator holds
         // 2^(13 - ex - 24) times the sum of q code; 2^ex and the rest (with the exponential's
         // argument) come back one after the other, since their product can leave fp32 where the
@@ -528,9 +527,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
         for (int e2 = 0; e2 < 2; ++e2) {
           const int src = 4 * (2 * c + e2);
           up_h[nt][e2] = __shfl_sync(0xffffffffu, up, src) * p.up_scale;
+          const float dn = __shfl_sync(0xffffffffu, down, src);
 #pragma unroll
           for (int gg = 0; gg < NG; ++gg)
-            qsum[gg][nt][e2] = __shfl_sync(0xffffffffu, sum[gg], src) * 5.9604644775390625e-8f;
+            qsum[gg][nt][e2] = __shfl_sync(0xffffffffu, sum[gg], src) * dn * 0x1p-17f;
         }
       }
     }
@@ -554,10 +554,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
       }
 
 #pragma unroll 1
-      for (int part = 0; part < NT; ++part) {
+      for (int part = 0; part < TU / TR; ++part) {
         const uint8_t* tile = whole + part * TR * U::BYTES;
         const int left = have - part * TR * page::kUnit;
-        if (NT > 1 && left <= 0) break;
+        if (TR < TU && left <= 0) break;
         // scores over the rest of their scale, x: x scale_log2 is in units of log2
         float x[TR][NT][4];
 #pragma unroll
@@ -753,73 +753,61 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
       issue(st);
     }
 
-    // ---- groups in doubt.  The groups share a reference, and a group whose steps are far below the
-    // other's has its weights among fp16's subnormals, each wrong by up to 2^-25.  A group is in
-    // doubt where, for any head, the sum of p s code over its 64 elements is so small that this could
-    // make up 2^-10 of their mean, codes being 15 at most.
-    unsigned few = 0u;
-    if constexpr (NG > 1) {
-      const float least = float((tw - t) / W * kTile) * (15.f * 64.f * 0x1p-15f * 0x1p-24f);
-      float sum[NG][NT][2], low = INFINITY;
+    // ---- join the warps' parts of this item: normalised outputs, log2 sums
+    if (tw - t >= W) {   // of the warps that had a tile
+      // Groups in doubt.  The groups share a reference, and a group whose steps are far below the
+      // other's has its weights among fp16's subnormals, each wrong by up to 2^-25.  A group is in
+      // doubt where any head's sum of p s code over a lane's 8 elements of it is so small that this
+      // could make up 2^-10 of it, codes being 15 at most.
+      unsigned few = 0u;
+      if constexpr (NG > 1) {
+        const float least = float((tw - t) / W * kTile) * (15.f * 8.f * 0x1p-15f * 0x1p-24f);
 #pragma unroll
-      for (int gg = 0; gg < NG; ++gg)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e2 = 0; e2 < 2; ++e2) {   // this lane's eight elements
-            auto two = [&](int i) { return oacc[gg][i][nt][e2] + oacc[gg][i][nt][2 + e2]; };
-            sum[gg][nt][e2] = two(0) + two(2) + 0.0625f * (two(1) + two(3));
-            low = fminf(low, sum[gg][nt][e2]);
-          }
-      if (!__all_sync(0xffffffffu, low >= least)) {
-#pragma unroll
-        for (int gg = 0; gg < NG; ++gg)
+        for (int gg = 0; gg < NG; ++gg) {
+          float low = INFINITY;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e2 = 0; e2 < 2; ++e2) {
-              float y = sum[gg][nt][e2];
-#pragma unroll
-              for (int o = 4; o < 32; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-              if (nt * 8 + 2 * c + e2 < nh && !(y >= least)) few |= 1u << gg;
+              auto two = [&](int i) { return oacc[gg][i][nt][e2] + oacc[gg][i][nt][2 + e2]; };
+              low = fminf(low, two(0) + two(2) + 0.0625f * (two(1) + two(3)));
             }
-        few = __reduce_or_sync(0xffffffffu, few);
-      }
-    }
-
-    // ---- join the warps' parts of this item: normalised outputs, log2 sums
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e2 = 0; e2 < 2; ++e2) {
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          l_run[nt][e2] += __shfl_xor_sync(0xffffffffu, l_run[nt][e2], o);
-#pragma unroll
-          for (int gg = 0; gg < NG; ++gg) om[gg][nt][e2] += __shfl_xor_sync(0xffffffffu, om[gg][nt][e2], o);
+          few |= __all_sync(0xffffffffu, low >= least) ? 0u : 1u << gg;
         }
-        const int h = nt * 8 + 2 * c + e2;
-        if (h < nh) {
-          const float l = l_run[nt][e2];
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          if (r == 0) s_l[warp * C::HEADS + h] = l == 0.f ? -INFINITY : ref[nt][e2] + log2f(l);
+      }
 #pragma unroll
-          for (int gg = 0; gg < NG; ++gg) {
-            const float add = om[gg][nt][e2] * inv;
-            const float lo = inv * 16777216.f, hi = inv * 1048576.f;   // undo the subnormals' 2^-24, 2^-20
-            float4* dst = reinterpret_cast<float4*>(s_o + (warp * C::HEADS + h) * D + gg * 64 + r * 8);
-            dst[0] = make_float4(fmaf(oacc[gg][0][nt][e2], lo, add), fmaf(oacc[gg][1][nt][e2], hi, add),
-                                 fmaf(oacc[gg][2][nt][e2], lo, add), fmaf(oacc[gg][3][nt][e2], hi, add));
-            dst[1] = make_float4(fmaf(oacc[gg][0][nt][2 + e2], lo, add), fmaf(oacc[gg][1][nt][2 + e2], hi, add),
-                                 fmaf(oacc[gg][2][nt][2 + e2], lo, add), fmaf(oacc[gg][3][nt][2 + e2], hi, add));
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            l_run[nt][e2] += __shfl_xor_sync(0xffffffffu, l_run[nt][e2], o);
+#pragma unroll
+            for (int gg = 0; gg < NG; ++gg) om[gg][nt][e2] += __shfl_xor_sync(0xffffffffu, om[gg][nt][e2], o);
+          }
+          const int h = nt * 8 + 2 * c + e2;
+          if (h < nh) {
+            const float l = l_run[nt][e2];
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            if (r == 0) s_l[warp * C::HEADS + h] = l == 0.f ? -INFINITY : ref[nt][e2] + log2f(l);
+#pragma unroll
+            for (int gg = 0; gg < NG; ++gg) {
+              const float add = om[gg][nt][e2] * inv;
+              const float lo = inv * 16777216.f, hi = inv * 1048576.f;   // undo the subnormals' 2^-24, 2^-20
+              float4* dst = reinterpret_cast<float4*>(s_o + (warp * C::HEADS + h) * D + gg * 64 + r * 8);
+              dst[0] = make_float4(fmaf(oacc[gg][0][nt][e2], lo, add), fmaf(oacc[gg][1][nt][e2], hi, add),
+                                   fmaf(oacc[gg][2][nt][e2], lo, add), fmaf(oacc[gg][3][nt][e2], hi, add));
+              dst[1] = make_float4(fmaf(oacc[gg][0][nt][2 + e2], lo, add), fmaf(oacc[gg][1][nt][2 + e2], hi, add),
+                                   fmaf(oacc[gg][2][nt][2 + e2], lo, add), fmaf(oacc[gg][3][nt][2 + e2], hi, add));
+            }
           }
         }
-      }
-    if constexpr (NG > 1) {
-      if (__builtin_expect(few != 0u, 0)) {   // behind the tile loop in the code: 2% of the call
-        __syncwarp();
-        plain_tiles<D>(p, p.q + ((long long)item.b * p.Hq + h0) * D, p.table + (long long)item.b * p.width, g, nh,
-                       item.j + (tw - t) % W, (tw - t) / W, W, L, few, s_o + warp * C::HEADS * D, s_l + warp * C::HEADS);
+      if constexpr (NG > 1) {
+        if (__builtin_expect(few != 0u, 0)) {   // behind the tile loop in the code: 2% of the call
+          __syncwarp();
+          plain_tiles<D>(p, p.q + ((long long)item.b * p.Hq + h0) * D, p.table + (long long)item.b * p.width, g, nh,
+                         item.j + (tw - t) % W, (tw - t) / W, W, L, few, s_o + warp * C::HEADS * D, s_l + warp * C::HEADS);
+        }
       }
     }
     __syncthreads();
