@@ -69,7 +69,7 @@ constexpr float kSmallStep = 3.2311742677852644e-27f;
 constexpr float kTopP = 1.2676506002282294e30f;
 constexpr float kTopMinimum = 1024.f;
 
-constexpr int kEvenSteps = 6;                     // log2: steps this far apart share a reference well
+constexpr int kEvenSteps = 6;                     // log2: steps this far below share the reference well
 constexpr int kMaxParts = 160;                   // blocks that can share a (sequence, kv head)
 
 // NT blocks of 8 heads per pass; a kv head with more than 8 query heads takes passes of 16, whose tiles
@@ -172,9 +172,9 @@ struct Cursor {
 
 // A warp's tiles of an item (ntile of them, from `tile` on, `every` apart) in plain fp32, where steps
 // of any size keep their part; some fifteen times slower than the products (48 sequences of 1-32K, 28
-// / 4 heads, all done again: 1.6 ms; four heads at a time 1.0, but 1% of every other call).  few: the groups in doubt.  Where all their steps are 0, or no token's
-// two steps are more than about 2^kEvenSteps apart, there is no doubt and nothing is done (35 us in
-// that case).  q: the heads' rows; row: the sequence's pages; out, out_l: normalised outputs [nh][D]
+// / 4 heads, all done again: 1.6 ms; four heads at a time 1.0, but 1% of every other call).  few: the groups in doubt.  Where all their steps are 0, or no token
+// has a step that is about 2^kEvenSteps below what its reference went by, there is no doubt and nothing
+// is done (35 us in that case).  q: the heads' rows; row: the sequence's pages; out, out_l: normalised outputs [nh][D]
 // and log2 sums [nh].
 template <int D>
 __device__ __forceinline__ void plain_tiles(const Params& p, const __nv_bfloat16* q, const int32_t* row, int g, int nh,
@@ -187,13 +187,16 @@ __device__ __forceinline__ void plain_tiles(const Params& p, const __nv_bfloat16
     if (pg < 0 || pg >= p.num_pages) pg = 0;            // recorded by the copies
     return p.pages + ((((long long)pg * p.Hkv + g) << upp_log) + (u & ((1 << upp_log) - 1))) * U::BYTES;
   };
-  unsigned seen = 0u;                                   // groups with a step above 0; steps far apart
+  unsigned seen = 0u;                                   // groups with a step above 0; a token like that
   for (int i = lane; i < ntile * kTile; i += 32) {
     const int t = (tile + i / kTile * every) * kTile + i % kTile;
     if (t >= L) break;
     const uint2 sm = *reinterpret_cast<const uint2*>(unit_at(t >> 4) + U::OFF_VS + (t & 15) * U::SCALE);
-    const int s0 = sm.x & 0xffffu, s1 = sm.y & 0xffffu;
-    seen |= (s0 ? 1u : 0u) | (s1 ? 2u : 0u) | (abs(s0 - s1) > kEvenSteps << 7 ? 4u : 0u);
+    // Exponents of the steps, and of what else the reference goes by (kMinimumShare, kSmallStep).
+    const int s0 = (sm.x >> 7) & 0xff, s1 = (sm.y >> 7) & 0xff;
+    const int other = max(max(int((sm.x >> 23) & 0xff), int((sm.y >> 23) & 0xff)) - 24, 127 - 88);
+    seen |= (sm.x & 0xffffu ? 1u : 0u) | (sm.y & 0xffffu ? 2u : 0u);
+    if ((sm.x | sm.y) != 0u && max(max(s0, s1), other) - min(s0, s1) > kEvenSteps) seen |= 4u;
   }
   seen = __reduce_or_sync(0xffffffffu, seen);
   if (!(seen & few) || !(seen & 4u)) return;

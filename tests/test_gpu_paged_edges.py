@@ -268,3 +268,22 @@ def test_prompt_attention_over_what_the_4bit_cache_keeps(D):
     rep = o_error_report(f64(bits_of(o)).reshape(o.shape), o_r, oa_r, nkeys=max(lens))
     assert rep["n_over_model"] == 0, rep
     assert np.abs(lse.double().cpu().numpy() - l_r).max() <= TOL_LSE
+
+
+@pytest.mark.parametrize("heads", [(7, 1), (12, 1)], ids=["7", "12"])
+@pytest.mark.parametrize("first", [0, 1])
+@pytest.mark.parametrize("size", [2.0 ** 20, 2.0 ** 60, 2.0 ** 90])
+def test_decode_4bit_a_token_of_large_equal_elements(heads, first, size):
+    """One token's groups are constant, and so large in one group that its minima set the softmax's
+    reference: the other group's outputs keep what the other tokens give them."""
+    from long_context_attention_fwd_b200 import ops
+    (Hq, Hkv), D, ps, lens = heads, 128, 16, [300, 40]
+    rng, q, kv = decode_inputs(lens, Hq, Hkv, D, 66)
+    for (_, v), at in zip(kv, (7, 39)):
+        v[at, 0, :] = 0.5
+        v[at, 0, 64 * first:64 * first + 64] = size
+    table, P = paged.table_for(rng, lens, ps)
+    pages, vals = pages4_of(kv, lens, table, P, ps, Hkv, D)
+    o, lse = ops.attn_decode_kv4(to_torch(q), dev(pages), dev(table), dev(np.array(lens, dtype=np.int32)))
+    ok_status()
+    check_decode4(o, lse, q, vals, lens, Hkv, D, 1 / math.sqrt(D))
