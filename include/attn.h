@@ -21,6 +21,7 @@
  *   - Grouped-query attention: query head h reads key/value head h / (Hq/Hkv).
  *   - causal != 0 masks key j for query i when j > i (positions within the sequence).
  *   - lse[i] = ln sum_j exp(scale * q_i . k_j) over the visible keys (natural log).
+ *   - scale is any finite number, negative ones and 0 too.
  *   - D must be 64 or 128; Hq must be a multiple of Hkv; B, Hq, Hkv, S >= 1.
  *   - Every tensor pointer is a device pointer owned by the caller; tensor pointers
  *     must be 16-byte aligned (lse and cu_seqlens 4-byte aligned).

@@ -63,7 +63,8 @@ constexpr uint32_t kTopWeight = 0x7400u;         // 2^14 as fp16: a weight this 
 constexpr float kFirstWeight = 6.f;              // ... so that the largest becomes 2^6
 // What else keeps p and p m inside fp32: a token counts in the reference with its steps, 2^-24 of
 // its minima (steps can be 0 where minima are not) and 2^-88 at least, and the reference also
-// moves when p reaches 2^100, or for every tile with a minimum of 2^10 or more.
+// moves when p reaches 2^100, or for every tile with a minimum of 2^10 or more.  (Next to a token
+// without steps or minima, weights below 2^-100 of its own are lost.)
 constexpr float kMinimumShare = 5.9604644775390625e-8f;
 constexpr float kSmallStep = 3.2311742677852644e-27f;
 constexpr float kTopP = 1.2676506002282294e30f;
