@@ -21,7 +21,7 @@
  *   - Grouped-query attention: query head h reads key/value head h / (Hq/Hkv).
  *   - causal != 0 masks key j for query i when j > i (positions within the sequence).
  *   - lse[i] = ln sum_j exp(scale * q_i . k_j) over the visible keys (natural log).
- *   - scale is any finite number, negative ones and 0 too.
+ *   - scale is any number from -2^127 to 2^127, 0 too.
  *   - D must be 64 or 128; Hq must be a multiple of Hkv; B, Hq, Hkv, S >= 1.
  *   - Every tensor pointer is a device pointer owned by the caller; tensor pointers
  *     must be 16-byte aligned (lse and cu_seqlens 4-byte aligned).
@@ -256,9 +256,9 @@ attn_status attn_decode_paged(const void* q, const void* k_pages, const void* v_
  * the products as exact integers and scores are summed in fp32; the weights, times V's
  * steps, are rounded to fp16 for the product with V's codes and summed unrounded (a group of 64
  * elements whose weights fp16 would lose next to the other group's is computed in fp32, some
- * fifteen times slower).  A table for 2^30 tiles of 64 tokens, a kv head and 16 query heads of it, or more,
- * is refused (eight are counted for the start of each).  Otherwise as attn_decode_paged (workspace
- * rules included). */
+ * fifteen times slower).  A table for 2^30 tiles of 64 tokens, a kv head and 16 query heads of it,
+ * or more, is refused (eight are counted for the start of each).  Otherwise as attn_decode_paged
+ * (workspace rules included). */
 size_t attn_decode_kv4_workspace_size(int B, int Hq, int Hkv, int D, int max_pages, int page_size);
 attn_status attn_decode_kv4(const void* q, const void* pages, const int32_t* block_table,
                             const int32_t* cache_len, void* o, float* lse, int B, int Hq, int Hkv,

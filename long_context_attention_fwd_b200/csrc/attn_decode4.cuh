@@ -31,8 +31,9 @@
 //      thousands of tokens has all the weight, of 2^13 or more where many share it.
 //
 // Work: the tiles (kTile tokens of one kv head) of all sequences form one line, with empty places
-// for each start, cut into equal parts, one per block, whatever the lengths.  A block's warps take its tiles in turn; each has
-// its own ring of asynchronous copies, its own reference, sum and output, and waits for nobody.
+// for each start, cut into equal parts, one per block, whatever the lengths.  A block's warps take
+// its tiles in turn; each has its own ring of asynchronous copies, its own reference, sum and output,
+// and waits for nobody.
 // (Copies are 16 bytes a lane: one bulk copy per unit, 2304 bytes, moved 4.3 TB/s at most, where
 // these alone move 6.4.)
 // At the end of a (sequence, kv head) the block's warps join theirs through shared memory; where
@@ -40,8 +41,8 @@
 // them (done flags with the call's tag, as attn_decode_kernel does).
 //
 // Measured, D = 128, 28 / 4 heads: 48 sequences of 1-32K tokens in pages of 16, 391 MB, 97 us
-// (4.0 TB/s, 62% of the copy rate); one of 32K, 14.4 us; one of 513, 9 us.  64 / 4 heads: 147 and
-// (16 / 1) 20.8 us.  The first fills no pipe (issue and ALU are active half of the time, tensor a
+// (4.0 TB/s, 62% of the copy rate); one of 32K, 14.4 us; one of 513, 9 us.  64 / 4 heads: 146 and
+// (16 / 1) 21.0 us.  The first fills no pipe (issue and ALU are active half of the time, tensor a
 // quarter): with two warps a scheduler, the copies, the conversions and the products largely add up
 // (when it took 102 us: without the copies 81, without the products 72, without both 44; an m16n8k16
 // holds its scheduler's issue for about 7 of its 8 cycles).  The others are latency: the length,
@@ -80,7 +81,7 @@ template <int D, int NT>
 struct Cfg {
   static constexpr int W = 8;                 // warps
   static constexpr int NS = 2;                // ring stages of a warp
-  static constexpr int TR = D == 128 ? kTileUnits / NT : kTileUnits;  // units with scores and weights in registers at a time
+  static constexpr int TR = D == 128 ? kTileUnits / NT : kTileUnits;  // units computed at a time
   static constexpr int THREADS = W * 32;
   static constexpr int HEADS = 8 * NT;
   static constexpr int TILE_BYTES = kTileUnits * page::Unit<D>::BYTES;
@@ -173,10 +174,11 @@ struct Cursor {
 
 // A warp's tiles of an item (ntile of them, from `tile` on, `every` apart) in plain fp32, where steps
 // of any size keep their part; some fifteen times slower than the products (48 sequences of 1-32K, 28
-// / 4 heads, all done again: 1.6 ms; four heads at a time 1.0, but 1% of every other call).  few: the groups in doubt.  Where all their steps are 0, or no token
-// has a step that is about 2^kEvenSteps below what its reference went by, there is no doubt and nothing
-// is done (35 us in that case).  q: the heads' rows; row: the sequence's pages; out, out_l: normalised outputs [nh][D]
-// and log2 sums [nh].
+// / 4 heads, all done again: 1.6 ms; four heads at a time 1.0, but 1% of every other call).  few: the
+// groups in doubt.  Where all their steps are 0, or no token has a step that is about 2^kEvenSteps
+// below what its reference went by, there is no doubt and nothing is done (35 us in that case).
+// q: the heads' rows; row: the sequence's pages; out, out_l: normalised outputs [nh][D] and log2
+// sums [nh].
 template <int D>
 __device__ __forceinline__ void plain_tiles(const Params& p, const __nv_bfloat16* q, const int32_t* row, int g, int nh,
                                             int tile, int ntile, int every, int L, unsigned few, float* out, float* out_l) {
@@ -318,9 +320,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) attn_decode4_kernel(co
   };
   // With few sequences and heads, or short ones and a block for each, each begins at a block of its
   // own: a block that ends one and begins the next would be last (28 / 4 heads, 1-600 tokens: 32
-  // sequences 9.0 us so; 33, which a lane each cannot hold, 15.7).  Otherwise every item has W places without tiles behind it on
-  // the line, what its start and its join cost (64 sequences of 1-600 tokens: 55 us without
-  // them, 19 with them).
+  // sequences 9.0 us so; 33, which a lane each cannot hold, 15.7).  Otherwise every item has W places
+  // without tiles behind it on the line, what its start and its join cost (64 sequences of 1-600
+  // tokens: 55 us without them, 19 with them).
   int chunk = max(share(), 1);  // 0 without a token in the batch
   const bool apart = p.B <= 32 && (4 * p.B * nv <= grid || (longest <= 2 * W && live <= grid));
   if (apart) {
